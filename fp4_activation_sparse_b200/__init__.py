@@ -17,6 +17,13 @@ Quantization for LLM Inference", Abstract):
   sharq_linear_grouped - the same for many experts (mixture of experts) in one launch
 and the library's dense FP4 baseline (the README's "NVFP4" mode):
   sharq_quantize_dense, sharq_linear_dense.
+
+The attention side of a served transformer block, between those linear layers:
+  sharq_kv_append    - per-head RMSNorm and rotation of q and k; k and v quantized into a paged
+                       FP4 cache (KVCache, KVBatch; alloc_kv_cache)
+  sharq_kv_read      - rows of that cache back as values
+  sharq_attention    - attention over it: single tokens, several, whole prompts
+  sharq_norm_residual - norms before and after a block, its gate, the scaled residual stream
 """
 from __future__ import annotations
 
@@ -53,13 +60,26 @@ class _WPack(ctypes.Structure):
                 ("n_out", ctypes.c_int), ("k", ctypes.c_int), ("fmt", ctypes.c_int)]
 
 
+class _KVCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("fmt", ctypes.c_int)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("n_seq", ctypes.c_int), ("max_pages", ctypes.c_int), ("max_q", ctypes.c_int),
+                ("tokens", ctypes.c_int)]
+
+
 def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: build it with `python -m fp4_activation_sparse_b200.build`")
     lib = ctypes.CDLL(path)
-    if not hasattr(lib, "sharq_dense_buffer_sizes"):
+    if not hasattr(lib, "sharq_dense_buffer_sizes") or not hasattr(lib, "sharq_norm_residual"):
         raise ImportError(f"{path} is stale (ABI older than this binding): rebuild it")
     P, I, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    L, KC, KB = ctypes.c_longlong, ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch)
     sig = {
         "sharq_prep_buffer_sizes": (S, [I, I, I, I, I, I, ctypes.POINTER(S)]),
         "sharq_dense_buffer_sizes": (S, [I, I, I, ctypes.POINTER(S)]),
@@ -77,6 +97,12 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sharq_quantize_dense": (I, [P, I, I, P, F, I, P, P, P]),
         "sharq_linear_dense": (I, [P, P, I, I, ctypes.POINTER(_WPack), P, I, P]),
         "sharq_rmsnorm": (I, [P, I, I, P, F, P, P]),
+        "sharq_kv_page_bytes": (S, [I, I, I, I]),
+        "sharq_kv_append": (I, [P, L, I, KC, KB, P, P, F, P, I, I, P, P]),
+        "sharq_kv_read": (I, [KC, KB, P, P, I, P]),
+        "sharq_attention_workspace_size": (S, [KC, KB, I]),
+        "sharq_attention": (I, [P, L, I, KC, KB, I, I, F, P, P, P, S, P]),
+        "sharq_norm_residual": (I, [P, P, I, I, P, P, I, I, F, P, F, P, P, P]),
         "sharq_mma_peak": (I, [I, I, I, I, P]),
         "sharq_device_status": (I, [P]),
         "sharq_set_wait_limit": (None, [ctypes.c_longlong]),
@@ -369,6 +395,270 @@ def sharq_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-6, out: 
     out = torch.empty_like(x) if out is None else out
     _check(lib.sharq_rmsnorm(_ptr(x), tokens, k, _ptr(gamma), float(eps), _ptr(out), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ the attention side of a block
+def _reject(message: str):
+    raise SharqError(SHARQ_ERR_INVALID_ARG, message)
+
+
+def _tensor(t, name: str, dtype, device, shape=None, contiguous: bool = True):
+    """Checks one device tensor argument (`shape` entries of None are free)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _reject(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        _reject(f"{name} must be {dtype} (got {t.dtype})")
+    if device is not None and t.device != device:
+        _reject(f"{name} is on {t.device}, the call on {device}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        _reject(f"{name} must have shape {tuple('any' if n is None else n for n in shape)} (got {tuple(t.shape)})")
+    if contiguous and not t.is_contiguous():
+        _reject(f"{name} must be contiguous")
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Distance in elements between the first-axis rows of `t`, which must itself be dense."""
+    n = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size > 1 and stride != n:
+            _reject(f"{name} may be strided along its first axis only")
+        n *= size
+    return t.stride(0) if t.shape[0] > 1 else n
+
+
+class _on:
+    """The tensors' device as the current one while a call runs."""
+
+    def __init__(self, device):
+        self.index, self.prev = device.index, None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.index:
+            self.prev = cur
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def sharq_kv_page_bytes(page_size: int, kv_heads: int, head_dim: int, fmt="nvfp4") -> int:
+    """Bytes of one page of the cache (all key heads)."""
+    n = lib.sharq_kv_page_bytes(page_size, kv_heads, head_dim, _fmt(fmt))
+    if n == 0:
+        raise SharqError(SHARQ_ERR_INVALID_ARG, last_error())
+    return n
+
+
+@dataclass(frozen=True, eq=False)
+class KVCache:
+    """A paged cache of FP4 keys and values: num_pages pages of page_size tokens in `pages`
+    (device bytes, num_pages * sharq_kv_page_bytes). k_scale, v_scale: float32 NVFP4 second-level
+    scales, one per key head (None: 1); MXFP4 has none."""
+    pages: torch.Tensor
+    num_pages: int
+    page_size: int
+    kv_heads: int
+    head_dim: int
+    fmt: int | str = "nvfp4"
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+    c: _KVCache = field(init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        need = self.num_pages * sharq_kv_page_bytes(self.page_size, self.kv_heads, self.head_dim, self.fmt)
+        _tensor(self.pages, "pages", torch.uint8, None)
+        if self.num_pages < 1 or self.pages.numel() < need:
+            _reject(f"{self.num_pages} pages need {need} bytes (got {self.pages.numel()})")
+        for name in ("k_scale", "v_scale"):
+            t = getattr(self, name)
+            if t is not None:
+                _tensor(t, name, torch.float32, self.pages.device)
+                if t.numel() != self.kv_heads:
+                    _reject(f"{name} must have one value per key head ({self.kv_heads}, got {t.numel()})")
+        if _fmt(self.fmt) == SHARQ_MXFP4 and (self.k_scale is not None or self.v_scale is not None):
+            _reject("MXFP4 has no second-level scales")
+        object.__setattr__(self, "c", _KVCache(
+            self.pages.data_ptr(), 0 if self.k_scale is None else self.k_scale.data_ptr(),
+            0 if self.v_scale is None else self.v_scale.data_ptr(), self.num_pages, self.page_size, self.kv_heads,
+            self.head_dim, _fmt(self.fmt)))
+
+
+@dataclass(frozen=True, eq=False)
+class KVBatch:
+    """One call's ragged batch (int32 device tensors): token rows [cu_q[b], cu_q[b+1]) are the
+    newest of sequence b, which has kv_len[b] tokens in the cache with them; position x lives in
+    page page_table[b, x // page_size]. max_q bounds the rows of one sequence; tokens is the row
+    count of the call's tensors (rows at or behind cu_q[-1] belong to no sequence: they are left
+    as they were). The tensors' contents are read when the kernels run and may change between
+    calls."""
+    cu_q: torch.Tensor
+    kv_len: torch.Tensor
+    page_table: torch.Tensor
+    max_q: int
+    tokens: int
+    c: _KVBatch = field(init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        _tensor(self.kv_len, "kv_len", torch.int32, None, (None,))
+        n = self.kv_len.numel()
+        _tensor(self.cu_q, "cu_q", torch.int32, self.kv_len.device, (n + 1,))
+        _tensor(self.page_table, "page_table", torch.int32, self.kv_len.device, (n, None))
+        object.__setattr__(self, "c", _KVBatch(self.cu_q.data_ptr(), self.kv_len.data_ptr(), self.page_table.data_ptr(),
+                                               n, self.page_table.shape[1], self.max_q, self.tokens))
+
+
+def alloc_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt="nvfp4",
+                   k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                   device="cuda") -> KVCache:
+    """A cache whose every value is zero."""
+    n = num_pages * sharq_kv_page_bytes(page_size, kv_heads, head_dim, fmt)
+    return KVCache(torch.zeros(n, dtype=torch.uint8, device=device), num_pages, page_size, kv_heads, head_dim, fmt,
+                   k_scale, v_scale)
+
+
+def _same_device(cache: KVCache, batch: KVBatch):
+    if batch.kv_len.device != cache.pages.device:
+        _reject(f"the batch is on {batch.kv_len.device}, the cache on {cache.pages.device}")
+    return cache.pages.device
+
+
+def sharq_kv_append(qkv: torch.Tensor, cache: KVCache, batch: KVBatch, q_heads: int,
+                    inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+                    q_gamma: torch.Tensor | None = None, k_gamma: torch.Tensor | None = None, eps: float = 1e-6,
+                    q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Append a call's keys and values. qkv bf16 [tokens, (q_heads + 2 kv_heads) * head_dim] (a
+    QKV projection's output; rows may be strided): q and k are normalized per head where gammas
+    are given, rotated by position * inv_freq (float32 [rot_dim/2]; None: no rotation), k and v
+    quantized into the cache. Returns the queries, bf16 [tokens, q_heads, head_dim]."""
+    dev = _same_device(cache, batch)
+    d, h = cache.head_dim, cache.kv_heads
+    _tensor(qkv, "qkv", torch.bfloat16, dev, (batch.tokens, (q_heads + 2 * h) * d), contiguous=False)
+    stride = _rows(qkv, "qkv")
+    for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+        if g is not None:
+            _tensor(g, name, torch.bfloat16, dev, (d,))
+    if inv_freq is not None:
+        _tensor(inv_freq, "inv_freq", torch.float32, dev, (None,))
+    if q_out is None:
+        q_out = torch.empty(batch.tokens, q_heads, d, dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(q_out, "q_out", torch.bfloat16, dev, (batch.tokens, q_heads, d))
+    with _on(dev):
+        _check(lib.sharq_kv_append(_ptr(qkv), stride, q_heads, ctypes.byref(cache.c), ctypes.byref(batch.c),
+                                   _ptr(q_gamma), _ptr(k_gamma), eps, _ptr(inv_freq),
+                                   0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), _ptr(q_out),
+                                   _stream(stream)))
+    return q_out
+
+
+def sharq_kv_read(cache: KVCache, batch: KVBatch, k_out: torch.Tensor | None = None,
+                  v_out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The batch's token rows of the cache as values: (k, v), [tokens, kv_heads, head_dim], bf16
+    or float32."""
+    dev = _same_device(cache, batch)
+    shape = (batch.tokens, cache.kv_heads, cache.head_dim)
+    if k_out is not None:
+        out_dtype = k_out.dtype
+    elif v_out is not None:
+        out_dtype = v_out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        _reject(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
+    k_out = torch.empty(shape, dtype=out_dtype, device=dev) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=out_dtype, device=dev) if v_out is None else v_out
+    _tensor(k_out, "k_out", out_dtype, dev, shape)
+    _tensor(v_out, "v_out", out_dtype, dev, shape)
+    with _on(dev):
+        _check(lib.sharq_kv_read(ctypes.byref(cache.c), ctypes.byref(batch.c), _ptr(k_out), _ptr(v_out),
+                                 SHARQ_OUT_F32 if out_dtype == torch.float32 else SHARQ_OUT_BF16, _stream(stream)))
+    return k_out, v_out
+
+
+def sharq_attention_workspace_size(cache: KVCache, batch: KVBatch, q_heads: int) -> int:
+    n = lib.sharq_attention_workspace_size(ctypes.byref(cache.c), ctypes.byref(batch.c), q_heads)
+    if n == 0:
+        raise SharqError(SHARQ_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def alloc_attention_workspace(cache: KVCache, batch: KVBatch, q_heads: int) -> torch.Tensor:
+    """A workspace for sharq_attention calls of this shape (zeroed once here; each call leaves it
+    ready for the next). Calls that may overlap on the GPU need one each."""
+    n = sharq_attention_workspace_size(cache, batch, q_heads)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.pages.device)
+
+
+def sharq_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, causal: bool = True, window: int = 0,
+                    scale: float | None = None, return_lse: bool = False, y: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q bf16 [tokens, q_heads, head_dim] (rows may be strided) over the cache:
+    y bf16 of q's shape, or (y, lse) with return_lse or an `lse` given (float32
+    [tokens, q_heads], the natural log of the sum of exponentials). `window` > 0 (causal only):
+    the last `window` positions. scale defaults to head_dim ** -0.5. `workspace` as from
+    alloc_attention_workspace (allocated here if omitted)."""
+    dev = _same_device(cache, batch)
+    d = cache.head_dim
+    _tensor(q, "q", torch.bfloat16, dev, (batch.tokens, None, d), contiguous=False)
+    hq = q.shape[1]
+    stride = _rows(q, "q")
+    if y is None:
+        y = torch.empty(batch.tokens, hq, d, dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(y, "y", torch.bfloat16, dev, (batch.tokens, hq, d))
+    if lse is not None:
+        _tensor(lse, "lse", torch.float32, dev, (batch.tokens, hq))
+    elif return_lse:
+        lse = torch.empty(batch.tokens, hq, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = alloc_attention_workspace(cache, batch, hq)
+    else:
+        _tensor(workspace, "workspace", torch.uint8, dev)
+    with _on(dev):
+        _check(lib.sharq_attention(_ptr(q), stride, hq, ctypes.byref(cache.c), ctypes.byref(batch.c), int(causal), window,
+                                   d ** -0.5 if scale is None else scale, _ptr(y), _ptr(lse), _ptr(workspace),
+                                   workspace.numel(), _stream(stream)))
+    return y if lse is None else (y, lse)
+
+
+def sharq_norm_residual(y: torch.Tensor, residual: torch.Tensor, post_gamma: torch.Tensor | None = None,
+                        gate: torch.Tensor | None = None, rows_per_gate: int = 0, alpha: float = 1.0,
+                        pre_gamma: torch.Tensor | None = None, eps: float = 1e-6,
+                        residual_out: torch.Tensor | None = None, h_out: torch.Tensor | None = None,
+                        stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """r' = bf16(alpha * residual + gate * norm(y)) and h = bf16(norm(r')): the norms after and
+    before a block (each only where its gamma [k] is given) with the block's gate ([k] or
+    [gate_rows, k]; token t uses row t // rows_per_gate, or row 0 when rows_per_gate is 0) and the
+    scaled residual stream. y, residual bf16 [tokens, k]. Returns (r', h); h is None without
+    pre_gamma. residual_out may be residual, h_out may be y."""
+    _tensor(y, "y", torch.bfloat16, None, (None, None))
+    tokens, k = y.shape
+    dev = y.device
+    _tensor(residual, "residual", torch.bfloat16, dev, (tokens, k))
+    for name, g in (("post_gamma", post_gamma), ("pre_gamma", pre_gamma)):
+        if g is not None:
+            _tensor(g, name, torch.bfloat16, dev, (k,))
+    gate_rows = 0
+    if gate is not None:
+        _tensor(gate, "gate", torch.bfloat16, dev, (k,) if gate.dim() == 1 else (None, k))
+        gate_rows = 1 if gate.dim() == 1 else gate.shape[0]
+    if residual_out is None:
+        residual_out = torch.empty_like(residual)
+    else:
+        _tensor(residual_out, "residual_out", torch.bfloat16, dev, (tokens, k))
+    if pre_gamma is None:
+        if h_out is not None:
+            _reject("h_out needs pre_gamma")
+    elif h_out is None:
+        h_out = torch.empty_like(residual)
+    else:
+        _tensor(h_out, "h_out", torch.bfloat16, dev, (tokens, k))
+    with _on(dev):
+        _check(lib.sharq_norm_residual(_ptr(y), _ptr(residual), tokens, k, _ptr(post_gamma), _ptr(gate), gate_rows,
+                                       rows_per_gate, alpha, _ptr(pre_gamma), eps, _ptr(residual_out), _ptr(h_out),
+                                       _stream(stream)))
+    return residual_out, h_out
 
 
 # flops one K step of one CTA pair performs in sharq_mma_peak, per mode: dense; sparse (logical,

@@ -2,6 +2,7 @@
 // Every entry point validates on the host before it launches anything and returns a
 // sharq_status; the message of the last failure is kept per host thread.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -9,6 +10,7 @@
 #include "../../include/sharq.h"
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
+#include "sharq_kv.h"
 
 namespace {
 
@@ -442,6 +444,216 @@ int sharq_rmsnorm(const void *x, int tokens, int k, const void *gamma, float eps
   cudaError_t e = sharq::launch_rmsnorm(static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(gamma), eps,
                                         tokens, k, static_cast<uint16_t *>(y), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "sharq_rmsnorm");
+  g_err[0] = 0;
+  return SHARQ_OK;
+}
+
+// Checks of the cache's and the batch's host-side fields; fill the kernels' views.
+static int check_kv_shape(int page_size, int kv_heads, int head_dim, int fmt) {
+  if (!valid_fmt(fmt)) return fail(SHARQ_ERR_INVALID_ARG, "unknown fmt %d", fmt);
+  if (page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)))
+    return fail(SHARQ_ERR_INVALID_ARG, "page_size must be a power of two in 16..4096 (got %d)", page_size);
+  if (kv_heads < 1 || kv_heads > 1024) return fail(SHARQ_ERR_INVALID_ARG, "kv_heads must be in 1..1024 (got %d)", kv_heads);
+  if (head_dim < 1) return fail(SHARQ_ERR_INVALID_ARG, "head_dim must be >= 1 (got %d)", head_dim);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(SHARQ_ERR_UNSUPPORTED, "head_dim %d is not executed; supported: 64, 128", head_dim);
+  return 0;
+}
+
+static int check_kv(const sharq_kv_cache *c, const sharq_kv_batch *b, sharq::KvCacheView *cv, sharq::KvBatchView *bv) {
+  if (!c || !b) return fail(SHARQ_ERR_INVALID_ARG, "null cache or batch");
+  if (int s = check_kv_shape(c->page_size, c->kv_heads, c->head_dim, c->fmt)) return s;
+  if (c->num_pages < 1) return fail(SHARQ_ERR_INVALID_ARG, "num_pages must be >= 1 (got %d)", c->num_pages);
+  if (!c->pages || !aligned16(c->pages)) return fail(SHARQ_ERR_INVALID_ARG, "pages must be a 16-byte aligned device buffer");
+  if (((uintptr_t)c->k_scale | (uintptr_t)c->v_scale) & 3u)
+    return fail(SHARQ_ERR_INVALID_ARG, "k_scale and v_scale must be 4-byte aligned");
+  if (c->fmt == SHARQ_MXFP4 && (c->k_scale || c->v_scale))
+    return fail(SHARQ_ERR_INVALID_ARG, "MXFP4 has no second-level scales: k_scale and v_scale must be null");
+  if (b->n_seq < 1 || b->n_seq > (1 << 20)) return fail(SHARQ_ERR_INVALID_ARG, "n_seq must be in 1..2^20 (got %d)", b->n_seq);
+  if (b->max_pages < 1 || (long long)b->max_pages * c->page_size > (1ll << 30))
+    return fail(SHARQ_ERR_INVALID_ARG, "max_pages must be >= 1 and cover at most 2^30 positions (got %d)", b->max_pages);
+  if (b->tokens < 0 || b->tokens > (1 << 28)) return fail(SHARQ_ERR_INVALID_ARG, "tokens must be in 0..2^28 (got %d)", b->tokens);
+  if (b->max_q < 0 || (b->max_q == 0 && b->tokens > 0))
+    return fail(SHARQ_ERR_INVALID_ARG, "max_q must be >= 1 where there are tokens (got %d)", b->max_q);
+  if (!b->cu_q || !b->kv_len || !b->page_table) return fail(SHARQ_ERR_INVALID_ARG, "null index array in the batch");
+  if (((uintptr_t)b->cu_q | (uintptr_t)b->kv_len | (uintptr_t)b->page_table) & 3u)
+    return fail(SHARQ_ERR_INVALID_ARG, "index arrays must be 4-byte aligned");
+  cv->pages = static_cast<uint8_t *>(c->pages);
+  cv->k_scale = c->k_scale;
+  cv->v_scale = c->v_scale;
+  cv->num_pages = c->num_pages;
+  cv->page_shift = 0;
+  while ((1 << cv->page_shift) < c->page_size) ++cv->page_shift;
+  cv->kv_heads = c->kv_heads;
+  bv->cu_q = b->cu_q;
+  bv->kv_len = b->kv_len;
+  bv->page_table = b->page_table;
+  bv->n_seq = b->n_seq;
+  bv->max_pages = b->max_pages;
+  bv->max_q = b->max_q < b->tokens ? b->max_q : b->tokens;
+  bv->tokens = b->tokens;
+  return 0;
+}
+
+static int check_heads(int q_heads, int kv_heads) {
+  if (q_heads < 1 || q_heads % kv_heads || q_heads / kv_heads > 128)
+    return fail(SHARQ_ERR_INVALID_ARG, "q_heads must be 1..128 times kv_heads (got %d and %d)", q_heads, kv_heads);
+  return 0;
+}
+
+size_t sharq_kv_page_bytes(int page_size, int kv_heads, int head_dim, int fmt) {
+  if (check_kv_shape(page_size, kv_heads, head_dim, fmt)) return 0;
+  return (size_t)kv_heads * (page_size / 16) * sharq::kv_group(head_dim, fmt).bytes;
+}
+
+int sharq_kv_append(const void *qkv, long long row_stride, int q_heads, const sharq_kv_cache *cache,
+                    const sharq_kv_batch *batch, const void *q_gamma, const void *k_gamma, float eps,
+                    const float *inv_freq, int rot_dim, int interleaved, void *q_out, void *stream) {
+  sharq::AppendParams p;
+  memset(&p, 0, sizeof p);
+  if (int s = check_kv(cache, batch, &p.c, &p.b)) return s;
+  if (int s = check_heads(q_heads, cache->kv_heads)) return s;
+  const int d = cache->head_dim;
+  if (rot_dim < 0 || rot_dim > d || rot_dim % 16)
+    return fail(SHARQ_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in 0..head_dim (got %d)", rot_dim);
+  if (rot_dim > 0 && (!inv_freq || ((uintptr_t)inv_freq & 3u)))
+    return fail(SHARQ_ERR_INVALID_ARG, "inv_freq must be a 4-byte aligned device array when rot_dim > 0");
+  if (row_stride < (long long)(q_heads + 2 * cache->kv_heads) * d || row_stride % 8)
+    return fail(SHARQ_ERR_INVALID_ARG, "row_stride must be a multiple of 8 that holds every head (got %lld)", row_stride);
+  if ((q_gamma || k_gamma) && !(eps >= 0.f)) return fail(SHARQ_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!aligned16(q_gamma) || !aligned16(k_gamma)) return fail(SHARQ_ERR_INVALID_ARG, "gammas must be 16-byte aligned");
+  if (batch->tokens == 0) {
+    g_err[0] = 0;
+    return SHARQ_OK;
+  }
+  if (!qkv || !q_out) return fail(SHARQ_ERR_INVALID_ARG, "null qkv or output");
+  if (!aligned16(qkv) || !aligned16(q_out)) return fail(SHARQ_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  p.qkv = static_cast<const uint16_t *>(qkv);
+  p.row_stride = row_stride;
+  p.q_gamma = static_cast<const uint16_t *>(q_gamma);
+  p.k_gamma = static_cast<const uint16_t *>(k_gamma);
+  p.inv_freq = inv_freq;
+  p.q_out = static_cast<uint16_t *>(q_out);
+  p.eps = eps;
+  p.q_heads = q_heads;
+  p.rot_half = rot_dim / 2;
+  p.interleaved = interleaved != 0;
+  cudaError_t e = sharq::launch_kv_append(p, d, cache->fmt, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "sharq_kv_append");
+  g_err[0] = 0;
+  return SHARQ_OK;
+}
+
+int sharq_kv_read(const sharq_kv_cache *cache, const sharq_kv_batch *batch, void *k_out, void *v_out, int out_dtype,
+                  void *stream) {
+  sharq::ReadParams p;
+  memset(&p, 0, sizeof p);
+  if (int s = check_kv(cache, batch, &p.c, &p.b)) return s;
+  if (out_dtype != SHARQ_OUT_BF16 && out_dtype != SHARQ_OUT_F32) return fail(SHARQ_ERR_INVALID_ARG, "bad out_dtype");
+  if (batch->tokens == 0) {
+    g_err[0] = 0;
+    return SHARQ_OK;
+  }
+  if (!k_out || !v_out) return fail(SHARQ_ERR_INVALID_ARG, "null output");
+  if (!aligned16(k_out) || !aligned16(v_out)) return fail(SHARQ_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.out_f32 = out_dtype == SHARQ_OUT_F32;
+  cudaError_t e = sharq::launch_kv_read(p, cache->head_dim, cache->fmt, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "sharq_kv_read");
+  g_err[0] = 0;
+  return SHARQ_OK;
+}
+
+static int attention_params(sharq::AttnParams *p, const sharq_kv_cache *cache, const sharq_kv_batch *batch, int q_heads) {
+  memset(p, 0, sizeof *p);
+  if (int s = check_kv(cache, batch, &p->c, &p->b)) return s;
+  if (int s = check_heads(q_heads, cache->kv_heads)) return s;
+  p->q_heads = q_heads;
+  p->group = q_heads / cache->kv_heads;
+  return 0;
+}
+
+size_t sharq_attention_workspace_size(const sharq_kv_cache *cache, const sharq_kv_batch *batch, int q_heads) {
+  sharq::AttnParams p;
+  if (attention_params(&p, cache, batch, q_heads)) return 0;
+  g_err[0] = 0;
+  return sharq::attention_workspace(p, cache->head_dim);
+}
+
+int sharq_attention(const void *q, long long q_stride, int q_heads, const sharq_kv_cache *cache,
+                    const sharq_kv_batch *batch, int causal, int window, float scale, void *y, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream) {
+  sharq::AttnParams p;
+  if (int s = attention_params(&p, cache, batch, q_heads)) return s;
+  const int d = cache->head_dim;
+  if (q_stride < (long long)q_heads * d || q_stride % 8)
+    return fail(SHARQ_ERR_INVALID_ARG, "q_stride must be a multiple of 8 that holds every head (got %lld)", q_stride);
+  if (window < 0 || (window > 0 && !causal))
+    return fail(SHARQ_ERR_INVALID_ARG, "window must be >= 0, and 0 without causal order (got %d)", window);
+  if (!std::isfinite(scale)) return fail(SHARQ_ERR_INVALID_ARG, "scale must be finite");
+  if ((uintptr_t)lse & 3u) return fail(SHARQ_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if (batch->tokens == 0) {
+    g_err[0] = 0;
+    return SHARQ_OK;
+  }
+  if (!q || !y) return fail(SHARQ_ERR_INVALID_ARG, "null q or output");
+  if (!aligned16(q) || !aligned16(y)) return fail(SHARQ_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  const size_t need = sharq::attention_workspace(p, d);
+  if (!workspace || workspace_bytes < need)
+    return fail(SHARQ_ERR_INVALID_ARG, "sharq_attention: this launch needs a workspace of %zu bytes (got %zu)", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned16(workspace)) return fail(SHARQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  p.q = static_cast<const uint16_t *>(q);
+  p.q_stride = q_stride;
+  p.y = static_cast<uint16_t *>(y);
+  p.lse = lse;
+  p.scale_log2 = scale * 1.44269504088896341f;
+  p.causal = causal != 0;
+  p.window = window;
+  p.workspace = static_cast<uint8_t *>(workspace);
+  cudaError_t e = sharq::launch_attention(p, d, cache->fmt, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "sharq_attention");
+  g_err[0] = 0;
+  return SHARQ_OK;
+}
+
+int sharq_norm_residual(const void *y, const void *residual, int tokens, int k, const void *post_gamma,
+                        const void *gate, int gate_rows, int rows_per_gate, float alpha, const void *pre_gamma,
+                        float eps, void *residual_out, void *h_out, void *stream) {
+  if (tokens < 0) return fail(SHARQ_ERR_INVALID_ARG, "tokens must be >= 0 (got %d)", tokens);
+  if (k < 8 || k % 8 || k > 32768)
+    return fail(SHARQ_ERR_INVALID_ARG, "k must be a positive multiple of 8, <= 32768 (got %d)", k);
+  if (rows_per_gate < 0 || gate_rows < 0) return fail(SHARQ_ERR_INVALID_ARG, "gate_rows and rows_per_gate must be >= 0");
+  if (gate && (gate_rows < 1 || (rows_per_gate > 0 && (long long)gate_rows * rows_per_gate < tokens)))
+    return fail(SHARQ_ERR_INVALID_ARG, "%d gate rows of %d tokens each do not cover %d tokens", gate_rows, rows_per_gate, tokens);
+  if ((post_gamma || pre_gamma) && !(eps >= 0.f)) return fail(SHARQ_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!std::isfinite(alpha)) return fail(SHARQ_ERR_INVALID_ARG, "alpha must be finite");
+  if (tokens == 0) {
+    g_err[0] = 0;
+    return SHARQ_OK;
+  }
+  if (!y || !residual || !residual_out || (pre_gamma && !h_out))
+    return fail(SHARQ_ERR_INVALID_ARG, "null y, residual or output");
+  if (!aligned16(y) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(h_out) || !aligned16(gate) ||
+      !aligned16(post_gamma) || !aligned16(pre_gamma))
+    return fail(SHARQ_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+  sharq::NormResidualParams p;
+  memset(&p, 0, sizeof p);
+  p.y = static_cast<const uint16_t *>(y);
+  p.post_gamma = static_cast<const uint16_t *>(post_gamma);
+  p.gate = static_cast<const uint16_t *>(gate);
+  p.residual = static_cast<const uint16_t *>(residual);
+  p.pre_gamma = static_cast<const uint16_t *>(pre_gamma);
+  p.residual_out = static_cast<uint16_t *>(residual_out);
+  p.h_out = static_cast<uint16_t *>(h_out);
+  p.alpha = alpha;
+  p.eps = eps;
+  p.tokens = tokens;
+  p.k = k;
+  p.rows_per_gate = rows_per_gate;
+  cudaError_t e = sharq::launch_norm_residual(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "sharq_norm_residual");
   g_err[0] = 0;
   return SHARQ_OK;
 }

@@ -1,0 +1,497 @@
+// Attention over the paged FP4 cache for few query rows per key head (decode, drafted tokens).
+//
+// For one key head the query rows are the group's heads of the call's new tokens: row
+// i * group + g. Scores and outputs are formed transposed, S^T = K Q^T and O^T = V^T P^T, so the
+// 16-row side of the matrix instruction holds keys and value elements and the 8-column side the
+// few query rows. Codes become float16 in registers: code * block scale is exact there (2 + 4
+// significant bits; the cache's E8M0 exponents are limited to float16's range), the second-level
+// scales and the softmax scale are applied in float32. Queries are scaled by a power of two per
+// row and are exact in float16 too. Probabilities are rounded to float16 (11 bits, against the
+// 8 of the bfloat16 output); their sum, the maxima and both accumulators are float32.
+#include "sharq_common.cuh"
+#include "sharq_kv.h"
+
+namespace sharq {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 32;   // keys per step of a warp: two groups of the cache
+constexpr int kStagesA = 3;  // tiles in flight per warp
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void lds64(uint32_t a, uint32_t *v) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
+}
+__device__ __forceinline__ void lds128(uint32_t a, uint32_t *v) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t trans8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// two scale codes in the low 16 bits -> half2 (low byte in the low half)
+template <bool MX>
+__device__ __forceinline__ uint32_t scales2(uint32_t two) {
+  uint32_t d;
+  if (MX) {
+    d = pack_half2(__uint_as_float((two & 0xFFu) << 23), __uint_as_float((two & 0xFF00u) << 15));
+  } else {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
+  }
+  return d;
+}
+// byte i (0..3, constant) of a word of codes -> half2 of its two values
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}"
+      : "=r"(d) : "r"(w), "n"(I));
+  return d;
+}
+
+template <int D, bool MX, int NT>
+struct RowsKernel {
+  static constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
+  static constexpr int R = 8 * NT;  // query rows of a block
+  static constexpr int KS = D / 16;  // matrix steps over D, and 16-row tiles of O^T
+  static constexpr int kStageBytes = 2 * G.bytes;
+  static constexpr int kRing = kWarps * kStagesA * kStageBytes;
+  static constexpr int kMerge = (kWarps / 2) * R * D * 4;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+};
+
+template <int D, bool MX, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel(const AttnParams p) {
+  using C = RowsKernel<D, MX, NT>;
+  constexpr KvLayout G = C::G;
+  constexpr int KS = C::KS;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float sh_m[kWarps][C::R], sh_l[kWarps][C::R];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int row_tiles = (p.b.max_q * p.group + C::R - 1) / C::R;
+  int w = blockIdx.x;
+  const int rt = w % row_tiles;
+  w /= row_tiles;
+  const int kh = w % p.c.kv_heads, seq = w / p.c.kv_heads;
+
+  const int q0 = __ldg(p.b.cu_q + seq), q_len = min(__ldg(p.b.cu_q + seq + 1) - q0, p.b.max_q);
+  const int kv_len = __ldg(p.b.kv_len + seq);
+  const int rows = min(q_len * p.group - rt * C::R, C::R);
+  if (rows <= 0) return;
+  const int first_pos = kv_len - (__ldg(p.b.cu_q + seq + 1) - q0);  // position of the sequence's first new token
+  const int pos_lo = first_pos + rt * C::R / p.group, pos_hi = first_pos + (rt * C::R + rows - 1) / p.group;
+  int k_lo = 0, k_hi = min(kv_len, p.b.max_pages << p.c.page_shift);  // no place behind the table
+  if (p.causal) {
+    k_hi = min(k_hi, pos_hi + 1);
+    if (p.window > 0) k_lo = max(0, pos_lo - p.window + 1);
+  }
+  const int t_lo = k_lo / kTile, t_hi = (max(k_hi, 0) + kTile - 1) / kTile;
+
+  // ---- query fragments: lane (g, t) holds elements [D/4 * t, D/4 * (t + 1)) of row g of each n tile
+  uint32_t qf[NT][KS][2];
+  float coef[NT][2];  // score factor of columns 2t, 2t+1: softmax scale, key scale, the row's power of two
+  const float ks = MX || !p.c.k_scale ? 1.f : __ldg(p.c.k_scale + kh);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = n * 8 + g, rr = rt * C::R + r;
+    const int token = q0 + rr / p.group, head = kh * p.group + rr % p.group;
+    uint32_t raw[KS * 2];
+    if (r < rows && token >= 0 && token < p.b.tokens) {
+      const uint16_t *src = p.q + (size_t)token * p.q_stride + head * D + t * (D / 4);
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+        raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) raw[i] = 0u;
+    }
+    float am = 0.f;
+#pragma unroll
+    for (int i = 0; i < KS * 2; ++i) am = max3abs(am, bf16lo(raw[i]), bf16hi(raw[i]));
+    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+    // the row's largest value moves to [2^12, 2^13): exact in float16 down to 2^-36 of it
+    const int e = max((int)(__float_as_uint(am) >> 23) - 127, -100);
+    const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < KS * 2; ++i) qf[n][i >> 1][i & 1] = pack_half2(bf16lo(raw[i]) * up, bf16hi(raw[i]) * up);
+    const float down = __uint_as_float((uint32_t)(127 - 12 + e) << 23) * ks * p.scale_log2;
+    coef[n][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
+    coef[n][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
+  }
+
+  float o[KS][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[i][n][q] = 0.f;
+  }
+
+  const uint32_t ring = smem_u32(smem) + warp * kStagesA * C::kStageBytes;
+  const int page_groups = 1 << (p.c.page_shift - 4);
+  const int *table = p.b.page_table + (size_t)seq * p.b.max_pages;
+  // page id of the group `gi` of the sequence, -1 where it holds no keys
+  auto page_of = [&](int gi) -> int {
+    const int col = gi >> (p.c.page_shift - 4);
+    if (16 * gi >= kv_len || col >= p.b.max_pages) return -1;
+    const int page = __ldg(table + col);
+    return page < p.c.num_pages ? page : -1;
+  };
+  // 16 tiles' page ids in the lanes: lane 2i + h has group h of the warp's tile base + i
+  int base = 0, ids = page_of(2 * (t_lo + warp + kWarps * (lane >> 1)) + (lane & 1));
+  auto tile_ids = [&](int i, int &a, int &b) {  // i-th tile of this warp (in increasing order of calls)
+    if (i - base >= 16) {
+      base += 16;
+      ids = page_of(2 * (t_lo + warp + kWarps * (base + (lane >> 1))) + (lane & 1));
+    }
+    a = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base));
+    b = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base) + 1);
+  };
+  const int my_tiles = t_hi - t_lo > warp ? (t_hi - t_lo - warp + kWarps - 1) / kWarps : 0;
+  uint32_t valid_bits = 0;  // bits 2s, 2s+1: the groups of ring stage s hold keys
+  auto load = [&](int i) {
+    if (i < my_tiles) {
+      int id[2];
+      tile_ids(i, id[0], id[1]);
+      const int s = i % kStagesA;
+      const int tile = t_lo + warp + kWarps * i;
+      valid_bits &= ~(3u << (2 * s));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (id[h] < 0) continue;  // warp-uniform
+        valid_bits |= 1u << (2 * s + h);
+        const uint8_t *src = p.c.pages + ((((size_t)id[h] * p.c.kv_heads + kh) << (p.c.page_shift - 4)) +
+                                          ((2 * tile + h) & (page_groups - 1))) * G.bytes;
+        const uint32_t dst = ring + s * C::kStageBytes + h * G.bytes;
+#pragma unroll
+        for (int c = 0; c < (G.bytes / 16 + 31) / 32; ++c)
+          if (c * 32 + lane < G.bytes / 16) cp_async16(dst + (c * 32 + lane) * 16, src + (size_t)(c * 32 + lane) * 16);
+      }
+    }
+    cp_commit();
+  };
+  for (int i = 0; i < kStagesA - 1; ++i) load(i);
+
+  for (int it = 0; it < my_tiles; ++it) {
+    __syncwarp();  // every lane has left the stage that the next load overwrites
+    load(it + kStagesA - 1);
+    cp_wait<kStagesA - 1>();
+    __syncwarp();
+    const int s = it % kStagesA;
+    const uint32_t st = ring + s * C::kStageBytes;
+    const int key0 = (t_lo + warp + kWarps * it) * kTile;
+    const uint32_t valid = (valid_bits >> (2 * s)) & 3u;
+
+    // ---- S^T: two 16-key tiles
+    float sc[2][NT][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sc[h][n][q] = 0.f;
+      uint32_t ca[KS / 2], cb[KS / 2];  // codes of rows g and g + 8: D/8 bytes from element D/4 * t
+      const uint32_t kc = st + h * G.bytes;
+      if (D == 128) {
+        lds128(kc + g * 64 + t * 16, ca);
+        lds128(kc + (g + 8) * 64 + t * 16, cb);
+      } else {
+        lds64(kc + g * 32 + t * 8, ca);
+        lds64(kc + (g + 8) * 32 + t * 8, cb);
+      }
+      // scales of the lane's elements: blocks of the first and second half of its matrix steps
+      uint32_t sa[2], sb[2];
+      const uint32_t kscale = kc + G.k_scales;
+      if (!MX && D == 128) {
+        const uint32_t a2 = scales2<MX>(lds16(kscale + g * 8 + 2 * t)), b2 = scales2<MX>(lds16(kscale + (g + 8) * 8 + 2 * t));
+        sa[0] = __byte_perm(a2, 0, 0x1010), sa[1] = __byte_perm(a2, 0, 0x3232);
+        sb[0] = __byte_perm(b2, 0, 0x1010), sb[1] = __byte_perm(b2, 0, 0x3232);
+      } else {
+        constexpr int NB = D / (MX ? 32 : 16);
+        const int blk = NB == 4 ? t : t >> 1;
+        const uint32_t two = scales2<MX>(lds8(kscale + g * NB + blk) | (lds8(kscale + (g + 8) * NB + blk) << 8));
+        sa[0] = sa[1] = __byte_perm(two, 0, 0x1010);
+        sb[0] = sb[1] = __byte_perm(two, 0, 0x3232);
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t wa = ca[k >> 1], wb = cb[k >> 1];
+        const uint32_t fa = sa[2 * k / KS], fb = sb[2 * k / KS];
+        uint32_t a[4];
+        if (k & 1) a[0] = code_pair<2>(wa), a[1] = code_pair<2>(wb), a[2] = code_pair<3>(wa), a[3] = code_pair<3>(wb);
+        else a[0] = code_pair<0>(wa), a[1] = code_pair<0>(wb), a[2] = code_pair<1>(wa), a[3] = code_pair<1>(wb);
+        a[0] = mul2(a[0], fa), a[1] = mul2(a[1], fb), a[2] = mul2(a[2], fa), a[3] = mul2(a[3], fb);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816(sc[h][n], a, qf[n][k][0], qf[n][k][1]);
+      }
+    }
+    // ---- scores in units of log2, masked
+    const bool whole = valid == 3u && key0 + kTile <= kv_len &&
+                       (!p.causal || (key0 + kTile - 1 <= pos_lo && (p.window <= 0 || key0 > pos_hi - p.window)));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sc[h][n][q] *= coef[n][q & 1];
+    if (!whole) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int pos = first_pos + (rt * C::R + n * 8 + 2 * t + c) / p.group;
+          const int hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
+          const int lo = p.causal && p.window > 0 ? pos - p.window : -1;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int key = key0 + 16 * h + g + 8 * q;
+              if (!((valid >> h) & 1u) || key > hi || key <= lo) sc[h][n][2 * q + c] = -INFINITY;
+            }
+        }
+    }
+    // ---- running maximum and sum
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+        const float top = fmaxf(m[n][c], mx);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float alpha = ex2(m[n][c] - ref);
+        m[n][c] = top;
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float e = ex2(sc[h][n][2 * q + c] - ref);
+            sc[h][n][2 * q + c] = e;
+            sum += e;
+          }
+        l[n][c] = l[n][c] * alpha + sum;
+        if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < KS; ++i) o[i][n][c] *= alpha, o[i][n][2 + c] *= alpha;
+        }
+      }
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!((valid >> h) & 1u)) continue;  // warp-uniform; its probabilities are zero
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        pf[n][0] = trans8x8(pack_half2(sc[h][n][0], sc[h][n][1]));
+        pf[n][1] = trans8x8(pack_half2(sc[h][n][2], sc[h][n][3]));
+      }
+      const uint32_t vc = st + h * G.bytes + G.v_codes;
+      uint32_t w[2][4];  // [slot half][words]: D = 128: key 2t {lo, hi}, key 2t+1 {lo, hi}
+      lds128(vc + lane * 16, w[0]);
+      if (D == 128) lds128(vc + 512 + lane * 16, w[1]);
+      constexpr int per_run = (MX ? 32 : 16) / (D / 8);  // runs that share a block: 1, 2 or 4
+      uint32_t vs = lds32(st + h * G.bytes + G.v_scales + (g / per_run * 4 + t) * 4);
+      const int left = kv_len - (key0 + 16 * h);  // keys of the group that exist
+      if (left < 16) {  // scales of the others may be anything: zero keeps 0 * v from NaN
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (8 * (q >> 1) + 2 * t + (q & 1) >= left) vs &= ~(0xFFu << (8 * q));
+      }
+      const uint32_t s0 = scales2<MX>(vs & 0xFFFFu), s1 = scales2<MX>(vs >> 16);
+      uint32_t even[2][2], odd[2][2];  // [word][slot half]: nibbles of two keys of one element per byte
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t a = D == 128 ? w[hh][x] : w[0][2 * hh], b = D == 128 ? w[hh][2 + x] : w[0][2 * hh + 1];
+          even[x][hh] = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+          odd[x][hh] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+        }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        uint32_t a[4];
+        const uint32_t e0 = even[i >> 2][0], e1 = even[i >> 2][1], o0 = odd[i >> 2][0], o1 = odd[i >> 2][1];
+        switch (i & 3) {
+          case 0: a[0] = code_pair<0>(e0), a[1] = code_pair<0>(o0), a[2] = code_pair<0>(e1), a[3] = code_pair<0>(o1); break;
+          case 1: a[0] = code_pair<1>(e0), a[1] = code_pair<1>(o0), a[2] = code_pair<1>(e1), a[3] = code_pair<1>(o1); break;
+          case 2: a[0] = code_pair<2>(e0), a[1] = code_pair<2>(o0), a[2] = code_pair<2>(e1), a[3] = code_pair<2>(o1); break;
+          default: a[0] = code_pair<3>(e0), a[1] = code_pair<3>(o0), a[2] = code_pair<3>(e1), a[3] = code_pair<3>(o1);
+        }
+        a[0] = mul2(a[0], s0), a[1] = mul2(a[1], s0), a[2] = mul2(a[2], s1), a[3] = mul2(a[3], s1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816(o[i][n], a, pf[n][0], pf[n][1]);
+      }
+    }
+  }
+  cp_wait<0>();
+
+  // ---- merge the warps: common maximum, then a tree of sums in a fixed order
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 4);
+      l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 8);
+      l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 16);
+      if (g == 0) sh_m[warp][n * 8 + 2 * t + c] = m[n][c], sh_l[warp][n * 8 + 2 * t + c] = l[n][c];
+    }
+  __syncthreads();
+  float top[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sh_m[x][n * 8 + 2 * t + c]);
+      top[n][c] = mm;
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) sum += sh_l[x][n * 8 + 2 * t + c] * ex2(sh_m[x][n * 8 + 2 * t + c] - ref);
+      l[n][c] = sum;
+      const float f = ex2(m[n][c] - ref);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[i][n][c] *= f, o[i][n][2 + c] *= f;
+    }
+  float *slots = reinterpret_cast<float *>(smem);
+#pragma unroll
+  for (int half = kWarps / 2; half > 0; half >>= 1) {
+    if (warp >= half && warp < 2 * half) {
+      float *dst = slots + (size_t)(warp - half) * C::R * D + lane;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dst[((i * NT + n) * 4 + q) * 32] = o[i][n][q];
+    }
+    __syncthreads();
+    if (warp < half) {
+      const float *src = slots + (size_t)warp * C::R * D + lane;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[i][n][q] += src[((i * NT + n) * 4 + q) * 32];
+    }
+    __syncthreads();
+  }
+  if (warp != 0) return;
+  const float vs = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + kh);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = n * 8 + 2 * t + c, rr = rt * C::R + r;
+      const int token = q0 + rr / p.group, head = kh * p.group + rr % p.group;
+      if (r >= rows || token < 0 || token >= p.b.tokens) continue;
+      const float inv = l[n][c] == 0.f ? 0.f : vs / l[n][c];  // a NaN query stays NaN
+      // the lane's run of D/8 elements: rows g (even elements) and g + 8 (odd) of each 16-row tile
+      uint32_t out[KS];
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[i][n][c] * inv, o[i][n][2 + c] * inv);
+        out[i] = *reinterpret_cast<const uint32_t *>(&h2);
+      }
+      uint16_t *dst = p.y + ((size_t)token * p.q_heads + head) * D + g * (D / 8);
+#pragma unroll
+      for (int i = 0; i < KS / 4; ++i)
+        reinterpret_cast<uint4 *>(dst)[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+      if (p.lse && g == 0)
+        p.lse[(size_t)token * p.q_heads + head] =
+            l[n][c] == 0.f ? -INFINITY : (top[n][c] + __log2f(l[n][c])) * 0.69314718055994531f;
+    }
+}
+
+template <int D, bool MX, int NT>
+cudaError_t launch_rows(const AttnParams &p, cudaStream_t st) {
+  using C = RowsKernel<D, MX, NT>;
+  auto kernel = attn_rows_kernel<D, MX, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long row_tiles = ((long long)p.b.max_q * p.group + C::R - 1) / C::R;
+  const long long blocks = row_tiles * p.c.kv_heads * p.b.n_seq;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  kernel<<<(unsigned)blocks, kWarps * 32, C::kSmem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, bool MX>
+cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
+  const long long rows = (long long)p.b.max_q * p.group;
+  if (rows <= 8) return launch_rows<D, MX, 1>(p, st);
+  if (rows <= 16) return launch_rows<D, MX, 2>(p, st);
+  return launch_rows<D, MX, 4>(p, st);
+}
+
+}  // namespace
+
+size_t attention_workspace(const AttnParams &, int) { return 16; }
+
+cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t st) {
+  if (d == 128) return fmt ? launch_d<128, true>(p, st) : launch_d<128, false>(p, st);
+  return fmt ? launch_d<64, true>(p, st) : launch_d<64, false>(p, st);
+}
+
+}  // namespace sharq

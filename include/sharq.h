@@ -285,6 +285,118 @@ int sharq_linear_dense(const void *tiles_dev, const float *row_scale_dev, int to
 int sharq_rmsnorm(const void *x_bf16_dev, int tokens, int k, const void *gamma_bf16_dev, float eps,
                   void *y_bf16_dev, void *stream);
 
+/* ------------------------------------------------------------------ attention side of a block
+ * Between the QKV projection and the o projection's preparation a served transformer rotates q
+ * and k, keeps k and v, and attends; between a projection and the next preparation it adds to the
+ * residual stream and normalizes. The calls below do that work on the library's FP4 formats: the
+ * keys and values live in a paged cache of E2M1 codes with NVFP4 or MXFP4 block scales. The pages
+ * have no counterpart; the formats and quantizers are those of the linear layer.
+ *
+ * Cache bytes. Page p, key head h: page_size/16 groups of 16 tokens, one contiguous run at byte
+ * ((p * kv_heads + h) * page_size/16) * G. With D = head_dim and B = 16 (NVFP4) or 32 (MXFP4), a
+ * group of G = 16 D + 32 D/B bytes holds, for its tokens r = 0..15:
+ *   K codes   byte r*D/2 + e/2, element e (the lower element in the low nibble)
+ *   V codes   from byte 8 D: with r = 8h + 2t + j (h, j in 0..1, t in 0..3), the elements
+ *             [g D/8, (g+1) D/8) in D/16 bytes at (64h + 2(4g + t) + j) * 8 (D = 128) or
+ *             (4(4g + t) + 2h + j) * 4 (D = 64)
+ *   K scales  from byte 16 D: byte r*D/B + block
+ *   V scales  from byte 16 D + 16 D/B: byte (4 block + t) * 4 + 2h + j
+ * Values: code * E4M3 block scale * the head's float32 second-level scale (NVFP4), or
+ * code * 2^(byte - 127) (MXFP4; the exponents are limited to -23..13 so that a value without the
+ * second-level scale is a float16 exactly). */
+typedef struct {
+  void *pages;          /* num_pages * sharq_kv_page_bytes bytes, 16-byte aligned */
+  const float *k_scale; /* [kv_heads] NVFP4 second-level scales (> 0), or NULL for 1 (MXFP4: NULL) */
+  const float *v_scale;
+  int num_pages, page_size; /* page_size: a power of two, 16..4096 tokens */
+  int kv_heads, head_dim;   /* head_dim 64 or 128 */
+  int fmt;                  /* sharq_fmt */
+} sharq_kv_cache;
+
+/* One call's ragged batch. Token rows [cu_q[b], cu_q[b+1]) belong to sequence b; they are its
+ * newest: token i of q_len has position kv_len[b] - q_len + i (non-causal attention aside, where
+ * positions do not matter). Position x of sequence b lives in page page_table[b][x / page_size],
+ * row x % page_size. A position past the table, or whose page id is negative or >= num_pages, has
+ * no place: appends to it are dropped, reads give zeros, attention does not see it. Rows at or
+ * behind cu_q[n_seq] (padding) belong to no sequence and are left as they were in every output.
+ * The index arrays are device memory, read when the kernels run (a captured call follows them). */
+typedef struct {
+  const int *cu_q;       /* [n_seq + 1], increasing (equal: a sequence without new tokens) */
+  const int *kv_len;     /* [n_seq] tokens of the sequence in the cache, the call's own included */
+  const int *page_table; /* [n_seq][max_pages] */
+  int n_seq, max_pages;
+  int max_q;             /* host bound: no sequence has more token rows in the call */
+  int tokens;            /* rows of the call's tensors, padding included */
+} sharq_kv_batch;
+
+/* Bytes of one page (all key heads); 0 (with sharq_last_error set) for invalid arguments. */
+size_t sharq_kv_page_bytes(int page_size, int kv_heads, int head_dim, int fmt);
+
+/* Append a call's keys and values (one launch).
+ *   qkv_bf16_dev  [tokens] rows of (q_heads + 2 kv_heads) * head_dim bf16: q heads, k heads, v
+ *                 heads (the QKV projection's output); row_stride elements apart (a multiple of 8)
+ *   q_gamma_bf16_dev, k_gamma_bf16_dev  [head_dim] RMSNorm weights of every q and k head, applied
+ *                 before the rotation, or NULL (each on its own)
+ *   inv_freq_dev  [rot_dim/2] float32: pair j of a head turns by position * inv_freq[j] (the
+ *                 angle, its sine and cosine in float64, rounded once to float32). rot_dim is a
+ *                 multiple of 16, <= head_dim, or 0 (inv_freq NULL: no rotation); elements past
+ *                 rot_dim are not turned.
+ *   interleaved   pairs (2j, 2j+1) instead of (j, j + rot_dim/2)
+ *   q_out_dev     [tokens][q_heads][head_dim] bf16: the normalized, rotated queries. May not
+ *                 overlap qkv.
+ * k (rotated, from float32) and v are quantized block by block, s the head's second-level scale:
+ *   NVFP4  sb = E4M3(amax * fp32(1/fp32(6 s))), code = E2M1(v * fp32(1/fp32(sb * s))), so that
+ *          values above 2688 s saturate; s in [2^-100, 2^100]
+ *   MXFP4  e = clamp(floor(log2 amax) - 2, -23, 13), code = E2M1(v * 2^-e)
+ * Two token rows of one call may not have the same place. A NaN takes no part in its block's
+ * maximum and is stored as the largest code. */
+int sharq_kv_append(const void *qkv_bf16_dev, long long row_stride, int q_heads, const sharq_kv_cache *cache,
+                    const sharq_kv_batch *batch, const void *q_gamma_bf16_dev, const void *k_gamma_bf16_dev,
+                    float eps, const float *inv_freq_dev, int rot_dim, int interleaved, void *q_out_dev,
+                    void *stream);
+
+/* Read the batch's token rows back as the values they stand for (one launch): prefix export,
+ * checks, calibration of the second-level scales.
+ *   k_out_dev, v_out_dev  [tokens][kv_heads][head_dim], bf16 (rounded once) or float32 */
+int sharq_kv_read(const sharq_kv_cache *cache, const sharq_kv_batch *batch, void *k_out_dev, void *v_out_dev,
+                  int out_dtype, void *stream);
+
+/* Attention of the batch's queries over the cache. Query head h reads key head
+ * h / (q_heads / kv_heads).
+ *   q_bf16_dev    [tokens][q_heads][head_dim] bf16, rows q_stride elements apart (a multiple of 8)
+ *   causal        token i sees the positions up to its own (the call's own keys must have been
+ *                 appended), and with window > 0 only the last `window` of them; otherwise every
+ *                 position below kv_len (window must be 0)
+ *   scale         factor of q . k (commonly 1/sqrt(head_dim)), finite
+ *   y_dev         [tokens][q_heads][head_dim] bf16
+ *   lse_dev       [tokens][q_heads] float32 natural log of the sum of exponentials, or NULL
+ *   workspace_dev device buffer of sharq_attention_workspace_size bytes, 16-byte aligned, ZEROED
+ *                 ONCE before its first use; each call leaves it ready for the next, of any shape
+ *                 that the buffer is large enough for. Calls whose launches may overlap on the GPU
+ *                 (captured graphs that replay at once among them) need distinct workspaces.
+ * A query that sees nothing gives y = 0 and lse = -inf. Scores, maxima, sums and outputs are
+ * float32; probabilities enter the value product as float16 relative to a running maximum. */
+size_t sharq_attention_workspace_size(const sharq_kv_cache *cache, const sharq_kv_batch *batch, int q_heads);
+int sharq_attention(const void *q_bf16_dev, long long q_stride, int q_heads, const sharq_kv_cache *cache,
+                    const sharq_kv_batch *batch, int causal, int window, float scale, void *y_dev, float *lse_dev,
+                    void *workspace_dev, size_t workspace_bytes, void *stream);
+
+/* Norms before and after a block, its gate and the scaled residual stream (one launch):
+ *   z  = y * rstd(y) * post_gamma          (y itself without post_gamma)
+ *   r' = bf16(alpha * residual + gate * z) (gate 1 without one)
+ *   h  = bf16(r' * rstd(r') * pre_gamma)   (r' as stored; no h without pre_gamma)
+ * rstd as sharq_rmsnorm. Products and sums are rounded float32 steps.
+ *   y, residual, residual_out, h_out  [tokens][k] bf16; residual_out may be residual and h_out
+ *                 may be y (in place); other overlaps are not allowed
+ *   post_gamma, pre_gamma  [k] bf16 or NULL
+ *   gate          [gate_rows][k] bf16 or NULL; row t uses gate row t / rows_per_gate (rows_per_gate
+ *                 0: every row uses row 0); gate_rows must cover every token
+ * k a positive multiple of 8, <= 32768; tokens >= 0. */
+int sharq_norm_residual(const void *y_bf16_dev, const void *residual_bf16_dev, int tokens, int k,
+                        const void *post_gamma_bf16_dev, const void *gate_bf16_dev, int gate_rows,
+                        int rows_per_gate, float alpha, const void *pre_gamma_bf16_dev, float eps,
+                        void *residual_out_dev, void *h_out_dev, void *stream);
+
 /* Diagnostic: the tensor-core ceiling that sharq_linear is measured against. The pages have no
  * counterpart; this is the measured denominator of the GEMM's tensor-pipe fraction. One
  * launch, one CTA pair per SM pair (or `clusters` pairs if 0 < clusters < SMs/2), each issuing
