@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsharq.so")
 SOURCES = ["sharq_api.cu", "sharq_prep.cu", "sharq_pack.cu", "sharq_gemm.cu", "sharq_norm.cu",
-           "sharq_kv.cu", "sharq_attn.cu", "sharq_block_norm.cu"]
+           "sharq_kv.cu", "sharq_attn.cu", "sharq_attn_tiles.cu", "sharq_block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -612,6 +612,8 @@ int sharq_attention(const void *q, long long q_stride, int q_heads, const sharq_
   p.causal = causal != 0;
   p.window = window;
   p.workspace = static_cast<uint8_t *>(workspace);
+  const long long lim = g_wait_limit.load(std::memory_order_relaxed);
+  p.limit_ns = lim > 0 ? (unsigned long long)lim : 4000000000ull;
   cudaError_t e = sharq::launch_attention(p, d, cache->fmt, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "sharq_attention");
   g_err[0] = 0;
@@ -674,8 +676,10 @@ int sharq_device_status(void *stream) {
   uint32_t prep_st = 0;
   cudaError_t e = sharq::read_and_clear_device_status(&st, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = sharq::read_and_clear_prep_status(&prep_st);
+  uint32_t attn_st = 0;
+  if (e == cudaSuccess) e = sharq::read_and_clear_attn_status(&attn_st);
   if (e != cudaSuccess) return cuda_fail(e, "sharq_device_status");
-  st |= (int)(prep_st << 1);
+  st |= (int)(prep_st << 1) | (int)(attn_st << 2);
   if (st) return fail(SHARQ_ERR_TIMEOUT, "a bounded device wait gave up (code 0x%x)", st);
   g_err[0] = 0;
   return SHARQ_OK;

@@ -10,6 +10,7 @@
 // 8 of the bfloat16 output); their sum, the maxima and both accumulators are float32.
 #include "sharq_common.cuh"
 #include "sharq_kv.h"
+#include "sharq_kv_device.cuh"
 
 namespace sharq {
 namespace {
@@ -18,9 +19,6 @@ constexpr int kWarps = 8;
 constexpr int kTile = 32;   // keys per step of a warp: two groups of the cache
 constexpr int kStagesA = 3;  // tiles in flight per warp
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -50,16 +48,6 @@ __device__ __forceinline__ void lds64(uint32_t a, uint32_t *v) {
 __device__ __forceinline__ void lds128(uint32_t a, uint32_t *v) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t trans8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -71,22 +59,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// two scale codes in the low 16 bits -> half2 (low byte in the low half)
-template <bool MX>
-__device__ __forceinline__ uint32_t scales2(uint32_t two) {
-  uint32_t d;
-  if (MX) {
-    d = pack_half2(__uint_as_float((two & 0xFFu) << 23), __uint_as_float((two & 0xFF00u) << 15));
-  } else {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
-  }
-  return d;
 }
 // byte i (0..3, constant) of a word of codes -> half2 of its two values
 template <int I>
@@ -165,7 +137,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
     const int e = max((int)(__float_as_uint(am) >> 23) - 127, -100);
     const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
 #pragma unroll
-    for (int i = 0; i < KS * 2; ++i) qf[n][i >> 1][i & 1] = pack_half2(bf16lo(raw[i]) * up, bf16hi(raw[i]) * up);
+    for (int i = 0; i < KS * 2; ++i) qf[n][i >> 1][i & 1] = kv_pack_half2(bf16lo(raw[i]) * up, bf16hi(raw[i]) * up);
     const float down = __uint_as_float((uint32_t)(127 - 12 + e) << 23) * ks * p.scale_log2;
     coef[n][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
     coef[n][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
@@ -182,7 +154,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       for (int q = 0; q < 4; ++q) o[i][n][q] = 0.f;
   }
 
-  const uint32_t ring = smem_u32(smem) + warp * kStagesA * C::kStageBytes;
+  const uint32_t ring = kv_smem_u32(smem) + warp * kStagesA * C::kStageBytes;
   const int page_groups = 1 << (p.c.page_shift - 4);
   const int *table = p.b.page_table + (size_t)seq * p.b.max_pages;
   // page id of the group `gi` of the sequence, -1 where it holds no keys
@@ -258,13 +230,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       uint32_t sa[2], sb[2];
       const uint32_t kscale = kc + G.k_scales;
       if (!MX && D == 128) {
-        const uint32_t a2 = scales2<MX>(lds16(kscale + g * 8 + 2 * t)), b2 = scales2<MX>(lds16(kscale + (g + 8) * 8 + 2 * t));
+        const uint32_t a2 = kv_scales2<MX>(lds16(kscale + g * 8 + 2 * t)), b2 = kv_scales2<MX>(lds16(kscale + (g + 8) * 8 + 2 * t));
         sa[0] = __byte_perm(a2, 0, 0x1010), sa[1] = __byte_perm(a2, 0, 0x3232);
         sb[0] = __byte_perm(b2, 0, 0x1010), sb[1] = __byte_perm(b2, 0, 0x3232);
       } else {
         constexpr int NB = D / (MX ? 32 : 16);
         const int blk = NB == 4 ? t : t >> 1;
-        const uint32_t two = scales2<MX>(lds8(kscale + g * NB + blk) | (lds8(kscale + (g + 8) * NB + blk) << 8));
+        const uint32_t two = kv_scales2<MX>(lds8(kscale + g * NB + blk) | (lds8(kscale + (g + 8) * NB + blk) << 8));
         sa[0] = sa[1] = __byte_perm(two, 0, 0x1010);
         sb[0] = sb[1] = __byte_perm(two, 0, 0x3232);
       }
@@ -317,14 +289,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
         const float top = fmaxf(m[n][c], mx);
         const float ref = top == -INFINITY ? 0.f : top;
-        const float alpha = ex2(m[n][c] - ref);
+        const float alpha = kv_ex2(m[n][c] - ref);
         m[n][c] = top;
         float sum = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const float e = ex2(sc[h][n][2 * q + c] - ref);
+            const float e = kv_ex2(sc[h][n][2 * q + c] - ref);
             sc[h][n][2 * q + c] = e;
             sum += e;
           }
@@ -341,8 +313,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       uint32_t pf[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        pf[n][0] = trans8x8(pack_half2(sc[h][n][0], sc[h][n][1]));
-        pf[n][1] = trans8x8(pack_half2(sc[h][n][2], sc[h][n][3]));
+        pf[n][0] = trans8x8(kv_pack_half2(sc[h][n][0], sc[h][n][1]));
+        pf[n][1] = trans8x8(kv_pack_half2(sc[h][n][2], sc[h][n][3]));
       }
       const uint32_t vc = st + h * G.bytes + G.v_codes;
       uint32_t w[2][4];  // [slot half][words]: D = 128: key 2t {lo, hi}, key 2t+1 {lo, hi}
@@ -356,7 +328,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
         for (int q = 0; q < 4; ++q)
           if (8 * (q >> 1) + 2 * t + (q & 1) >= left) vs &= ~(0xFFu << (8 * q));
       }
-      const uint32_t s0 = scales2<MX>(vs & 0xFFFFu), s1 = scales2<MX>(vs >> 16);
+      const uint32_t s0 = kv_scales2<MX>(vs & 0xFFFFu), s1 = kv_scales2<MX>(vs >> 16);
       uint32_t even[2][2], odd[2][2];  // [word][slot half]: nibbles of two keys of one element per byte
 #pragma unroll
       for (int x = 0; x < D / 64; ++x)
@@ -407,9 +379,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       const float ref = mm == -INFINITY ? 0.f : mm;
       float sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x) sum += sh_l[x][n * 8 + 2 * t + c] * ex2(sh_m[x][n * 8 + 2 * t + c] - ref);
+      for (int x = 0; x < kWarps; ++x) sum += sh_l[x][n * 8 + 2 * t + c] * kv_ex2(sh_m[x][n * 8 + 2 * t + c] - ref);
       l[n][c] = sum;
-      const float f = ex2(m[n][c] - ref);
+      const float f = kv_ex2(m[n][c] - ref);
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][n][c] *= f, o[i][n][2 + c] *= f;
     }
@@ -490,6 +462,8 @@ cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
 size_t attention_workspace(const AttnParams &, int) { return 16; }
 
 cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t st) {
+  // 32 rows: what one block of the kernel above can hold in registers
+  if ((long long)p.b.max_q * p.group > 32) return launch_attention_tiles(p, d, fmt, st);
   if (d == 128) return fmt ? launch_d<128, true>(p, st) : launch_d<128, false>(p, st);
   return fmt ? launch_d<64, true>(p, st) : launch_d<64, false>(p, st);
 }

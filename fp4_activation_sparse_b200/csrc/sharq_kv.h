@@ -78,6 +78,7 @@ struct AttnParams {
   int q_heads, group;  // group = q_heads / kv_heads
   int causal, window;  // window 0: none
   uint8_t *workspace;
+  unsigned long long limit_ns;  // of the bounded waits
   KvBatchView b;
   KvCacheView c;
 };
@@ -92,6 +93,8 @@ struct NormResidualParams {
 cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t launch_kv_read(const ReadParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t st);
+cudaError_t launch_attention_tiles(const AttnParams &p, int d, int fmt, cudaStream_t st);
+cudaError_t read_and_clear_attn_status(uint32_t *status);
 size_t attention_workspace(const AttnParams &p, int d);
 cudaError_t launch_norm_residual(const NormResidualParams &p, cudaStream_t st);
 
