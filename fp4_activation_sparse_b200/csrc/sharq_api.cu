@@ -571,6 +571,9 @@ static int attention_params(sharq::AttnParams *p, const sharq_kv_cache *cache, c
   if (int s = check_heads(q_heads, cache->kv_heads)) return s;
   p->q_heads = q_heads;
   p->group = q_heads / cache->kv_heads;
+  if ((unsigned long long)p->b.max_q * p->group * p->group >= 1ull << 32)
+    return fail(SHARQ_ERR_UNSUPPORTED, "max_q * (q_heads / kv_heads)^2 must be below 2^32 (got %d and %d)", p->b.max_q, p->group);
+  p->group_inv = (uint32_t)(((1ull << 32) + p->group - 1) / p->group);
   return 0;
 }
 

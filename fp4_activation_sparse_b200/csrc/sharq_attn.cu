@@ -459,11 +459,15 @@ cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
 
 }  // namespace
 
-size_t attention_workspace(const AttnParams &, int) { return 16; }
+namespace {
+// 32 rows: what one block of the kernel above can hold in registers
+bool use_tiles(const AttnParams &p) { return (long long)p.b.max_q * p.group > 32; }
+}  // namespace
+
+size_t attention_workspace(const AttnParams &p, int d) { return use_tiles(p) ? attention_tiles_workspace(p, d) : 16; }
 
 cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t st) {
-  // 32 rows: what one block of the kernel above can hold in registers
-  if ((long long)p.b.max_q * p.group > 32) return launch_attention_tiles(p, d, fmt, st);
+  if (use_tiles(p)) return launch_attention_tiles(p, d, fmt, st);
   if (d == 128) return fmt ? launch_d<128, true>(p, st) : launch_d<128, false>(p, st);
   return fmt ? launch_d<64, true>(p, st) : launch_d<64, false>(p, st);
 }

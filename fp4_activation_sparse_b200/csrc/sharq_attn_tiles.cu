@@ -11,14 +11,28 @@
 //   warps 0..3, 4..7  softmax of tile 0 and of tile 1, one row per thread: maximum, exponentials
 //                     (float32; rounded to float16 only as the operand P), sum, and the rescaling
 //                     of O. O is rescaled only where a row's maximum grew by more than 2^8 since the
-//                     last time: exponentials then stay below 2^8, far inside float16's range.
+//                     last time: exponentials then stay below 2^8, far inside float16's range. They
+//                     also bring the queries into shared memory, the next segment's before this
+//                     one's output is read, so that its first scores form meanwhile.
 //   warps 8..11       codes and scales from global memory (the next tile's are in flight in
 //                     registers), float16 into the shared-memory tiles
-//   warp 12           tensor memory, and one thread that issues every MMA
-// The two tiles alternate on the tensor pipe: while one tile's exponentials are formed, the other
-// tile's products run. Every mbarrier wait is bounded; on expiry the block records a status word,
-// stops issuing, waits for what it issued, frees its tensor memory and exits.
+//   warps 12, 13      one thread each that issues the MMAs of tile 0 and of tile 1 (12: tensor memory)
+//   warp 14           the block's work list
+// A step's keys come in two halves with a score buffer each, so that the scores of the next half
+// form while this half's exponentials do, and the softmax warps never wait for the tensor pipe's
+// latency; while one tile's exponentials are formed, the other tile's products run.
+//
+// The grid is one block per SM, and every block takes an equal, contiguous share of all key steps
+// of the launch (found from the device's own lengths), so ragged batches balance and few long
+// sequences fill the GPU. Within its share a block goes from segment to segment without draining:
+// the queries of the next one load and its first keys are converted while the last step of this
+// one is in its softmax. A query block whose steps are cut between blocks leaves its parts (O, m, l
+// in float32) in the workspace; the block that arrives last joins them in the order of the keys.
+//
+// Every mbarrier wait is bounded; on expiry the block records a status word, stops issuing, waits
+// for what it issued, frees its tensor memory and exits.
 #include "sharq_common.cuh"
+#include "sharq_internal.h"
 #include "sharq_kv.h"
 #include "sharq_kv_device.cuh"
 
@@ -31,7 +45,7 @@ namespace {
 constexpr int kRows = 128;  // query rows of a tile
 constexpr int kKeys = 128;  // keys of a step
 constexpr int kThreads = 512;
-constexpr uint32_t kTmemCols = 512;  // S0, S1 at 0 and 128; O0, O1 at 256 and 384
+constexpr uint32_t kTmemCols = 512;  // S of tile t, half h at 128 t + 64 h (P over its first 32); O at 256 + 128 t
 constexpr uint64_t kDrainLimitNs = 4000000000ull;
 constexpr int kValidRing = 4;
 
@@ -45,14 +59,21 @@ struct TileSmem {
 };
 
 struct Bars {
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t work_full[2], work_empty[2], q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_empty[2], drain[2];  // [row tile][half of a step]
 };
+constexpr int kWorkReaders = 8 + 4 + 2;  // warps
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// one arrival for the warp, after all its lanes
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -70,24 +91,34 @@ __device__ __forceinline__ uint64_t globaltimer() {
 }
 // Gives up after `limit_ns`, or when another role of the block already did.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t *abort_flag) {
-  if (mbar_try(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if (i == 1 || (i & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (globaltimer() - t0 > limit_ns) {
-        *abort_flag = 1u;
-        atomicOr(&g_attn_status, 1u);
-        return false;
-      }
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
+    if (i & 31u) continue;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit_ns) {
+      *abort_flag = 1u;
+      atomicOr(&g_attn_status, 1u);
     }
+    if (*abort_flag) return false;
   }
+  return true;
 }
-// the same in every lane with a vote, for warps that run aligned instructions afterwards
+// the same for a whole warp, which leaves the wait together
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                                volatile uint32_t *abort_flag) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit_ns, abort_flag)) != 0;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !__all_sync(0xFFFFFFFFu, mbar_try(bar, parity)); ++i) {
+    if (i & 31u) continue;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit_ns) {
+      *abort_flag = 1u;
+      atomicOr(&g_attn_status, 1u);
+    }
+    if (__any_sync(0xFFFFFFFFu, *abort_flag != 0)) return false;
+  }
+  return true;
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -103,27 +134,31 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 // Rows along the outer dimension (Q, K: contraction contiguous): 8-row groups 1024 bytes apart.
 // V is stored [key][element], so its contraction runs over the rows: 64-element slabs kSlab bytes
 // apart (leading offset), 8-key groups 1024 bytes apart (stride offset).
-constexpr uint64_t desc_template(uint32_t lbo, uint32_t sbo) {
-  return ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-constexpr uint64_t kDescK = desc_template(16, 1024), kDescV = desc_template(16384, 1024);
-__device__ __forceinline__ uint64_t desc(uint64_t tmpl, uint32_t addr) { return tmpl | (uint64_t)((addr >> 4) & 0x3FFFu); }
+constexpr uint32_t desc_high(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+constexpr uint32_t kDescHigh = desc_high(1024);
+__device__ __forceinline__ uint32_t desc_low(uint32_t lbo, uint32_t addr) { return (lbo >> 4) << 16 | (addr >> 4); }
 
 // kind::f16 instruction descriptor: float16 operands, float32 accumulator, M = 128
 constexpr uint32_t idesc_f16(int n, bool b_outer_contiguous) {
   return (1u << 4) | ((b_outer_contiguous ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// operands by the lower words of their descriptors
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHigh)
       : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 #define SHARQ_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
@@ -144,26 +179,58 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t *v) {
       : "memory");
 }
 
+// the n lowest bits (none for n <= 0, all for n >= 32)
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// pairs of float32
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-// What the block works on; every role computes it alike.
+// row / group for row < 2^32 / group (launch_attention's callers keep to that)
+__device__ __forceinline__ int over_group(const AttnParams &p, int row) { return (int)__umulhi((uint32_t)row, p.group_inv); }
+__device__ __forceinline__ int token_of(const AttnParams &p, int row) { return p.group == 1 ? row : over_group(p, row); }
+
+// ---------------------------------------------------------------- what a block works on
+// An item is 256 query rows of one key head of one sequence; an entry is an item of every head
+// (they cost the same). Steps of all items in a row, entry by entry, are cut into equal shares.
+// An item costs its key steps and kItemCost more (queries in, output out, the pipeline's start:
+// measured at about two steps); a share's place inside the first kItemCost units is its first step.
+constexpr int kItemCost = 2;
+struct Range {
+  int q0, rows, kv_len, first_pos, row0;
+  int lo[2], hi[2];  // key steps of each row tile; lo >= hi: none
+  int begin, end;    // of the item
+  __device__ __forceinline__ int cost() const { return rows <= 0 ? 0 : kItemCost + max(1, end - begin); }
+};
 struct Work {
-  int q0, rows, kh, kv_len, first_pos, row0;
-  int lo[2], hi[2];  // key tiles of each row tile; lo >= hi: none
-  int begin, end;    // key tiles of the block
+  Range r;  // lo, hi, begin, end limited to the segment
+  int seq, kh;
+  int parts, part, owner;  // segments of the item, this one's place, the block of the first
 };
 
-__device__ __forceinline__ Work block_work(const AttnParams &p) {
-  Work w;
-  const int per = p.b.n_seq * p.c.kv_heads;
-  const int row_tiles = (int)(((long long)p.b.max_q * p.group + 2 * kRows - 1) / (2 * kRows));
-  const int rt = row_tiles - 1 - (int)(blockIdx.x / per);  // causal order: the longest first
-  const int seq = (blockIdx.x % per) / p.c.kv_heads;
-  w.kh = blockIdx.x % p.c.kv_heads;
+__device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt) {
+  Range w;
   const int q1 = __ldg(p.b.cu_q + seq + 1);
   w.q0 = __ldg(p.b.cu_q + seq);
   w.kv_len = __ldg(p.b.kv_len + seq);
@@ -177,8 +244,8 @@ __device__ __forceinline__ Work block_work(const AttnParams &p) {
     int k_lo = 0, k_hi = reach;
     const int last = min(w.rows, (t + 1) * kRows) - 1;
     if (p.causal) {
-      k_hi = min(k_hi, w.first_pos + (w.row0 + max(last, 0)) / p.group + 1);
-      if (p.window > 0) k_lo = max(0, w.first_pos + (w.row0 + t * kRows) / p.group - p.window + 1);
+      k_hi = min(k_hi, w.first_pos + token_of(p, w.row0 + max(last, 0)) + 1);
+      if (p.window > 0) k_lo = max(0, w.first_pos + token_of(p, w.row0 + t * kRows) - p.window + 1);
     }
     w.lo[t] = k_lo / kKeys;
     w.hi[t] = last >= t * kRows ? (max(k_hi, 0) + kKeys - 1) / kKeys : 0;
@@ -186,6 +253,91 @@ __device__ __forceinline__ Work block_work(const AttnParams &p) {
   }
   if (w.end == 0) w.begin = 0;
   return w;
+}
+
+// Where a block's share begins and ends, in steps and as an entry with its first step.
+struct Share {
+  long long total, blocks;  // steps of the launch, blocks that have a share
+  long long cut[2];         // begin and end of the share
+  long long first;          // first step of the entry that the share begins in
+  int entry, snap;
+};
+
+// A cut is moved to the item's edge where it would leave a piece of `snap` steps or fewer
+// (so that a cut inside an item always stands behind its first kItemCost units).
+__device__ __forceinline__ long long raw_cut(const Share &s, long long block) {
+  return block >= s.blocks ? s.total : block * s.total / s.blocks;
+}
+__device__ __forceinline__ long long snapped(long long x, long long p0, long long p1, int snap) {
+  return x - p0 <= kItemCost + snap ? p0 : p1 - x <= snap ? p1 : x;
+}
+
+// All threads: the entries' costs are summed in chunks of the block size, then the entries that
+// hold the share's two ends are found (from registers where one chunk holds every entry).
+__device__ __forceinline__ void find_share(const AttnParams &p, int row_tiles, Share *sh, long long *warp_sums) {
+  const long long entries = (long long)p.b.n_seq * row_tiles;
+  const int heads = p.c.kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long total = 0, before = 0, cost = 0, e = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+    for (long long e0 = 0; e0 < entries; e0 += kThreads) {
+      if (pass == 0 || entries > kThreads) {
+        e = e0 + threadIdx.x;
+        cost = e < entries ? (long long)item_range(p, (int)(e / row_tiles), (int)(e % row_tiles)).cost() * heads : 0;
+        long long inc = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+          if (lane >= o) inc += up;
+        }
+        __syncthreads();  // the sums of the chunk before have been read
+        if (lane == 31) warp_sums[warp] = inc;
+        __syncthreads();
+        before = base + inc - cost;
+        for (int x = 0; x < kThreads / 32; ++x) {
+          const long long v = warp_sums[x];
+          if (x < warp) before += v;
+          base += v;
+        }
+      }
+      if (pass == 1 && cost > 0) {
+        const int item = (int)(cost / heads);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const long long x = raw_cut(*sh, (long long)blockIdx.x + i);
+          if (x < before || x >= before + cost) continue;
+          const long long p0 = before + (x - before) / item * item;
+          const long long at = snapped(x, p0, p0 + item, sh->snap);
+          sh->cut[i] = at;
+          if (i == 0) sh->entry = (int)e, sh->first = before;
+        }
+      }
+    }
+    if (pass == 0) {
+      total = base;
+      if (threadIdx.x == 0) {
+        sh->total = total;
+        sh->blocks = min((long long)gridDim.x, max(1ll, total / (kItemCost + 2)));  // at least two steps each
+        sh->snap = (int)min(2ll, total / sh->blocks / 4);
+        sh->cut[0] = sh->cut[1] = total;  // ends that no entry holds
+        sh->entry = 0, sh->first = 0;
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+}
+
+// The part of the item [p0, p1) that begins at `from`: how many parts it has, which one this is and
+// the block that holds the first.
+__device__ __forceinline__ void item_parts(const Share &s, long long p0, long long p1, long long from, Work &w) {
+  // cuts strictly inside: block numbers c with p0 + kItemCost + snap < raw_cut(c) < p1 - snap
+  const long long lo = ((p0 + kItemCost + s.snap + 1) * s.blocks + s.total - 1) / s.total;
+  long long hi = ((p1 - s.snap) * s.blocks + s.total - 1) / s.total - 1;
+  hi = min(hi, s.blocks - 1);
+  w.parts = hi >= lo ? (int)(hi - lo + 2) : 1;
+  w.owner = (int)lo - 1;
+  w.part = from == p0 ? 0 : (int)(blockIdx.x - lo + 1);
 }
 
 // ---------------------------------------------------------------- codes to float16 tiles
@@ -294,38 +446,138 @@ __device__ __forceinline__ void store_v(uint32_t tile, int row0, int lane, int l
   }
 }
 
+// Entry n of the work list; every warp hands it back when it has read what it needs.
+__device__ __forceinline__ bool get_work(Bars &bars, const Work *ring, int n, uint64_t limit, volatile uint32_t *abort_flag) {
+  return mbar_wait_warp(kv_smem_u32(&bars.work_full[n & 1]), (n >> 1) & 1, limit, abort_flag) && ring[n & 1].r.rows > 0;
+}
+__device__ __forceinline__ void done_work(Bars &bars, int n) {
+  mbar_arrive_warp(kv_smem_u32(&bars.work_empty[n & 1]));
+}
+
+__device__ __forceinline__ void st256(void *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), SHARQ_I8(v, 0) : "memory");
+}
+
+// The share's next segment (rows 0: none is left). One thread; the walk's state stays in `sh`.
+__device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles, Share &sh, Work &out) {
+  const int heads = p.c.kv_heads;
+  const long long at = sh.cut[0];
+  out.r.rows = 0;
+  if (at >= sh.cut[1]) return;
+  Work x;
+  int cost;
+  long long first = sh.first;
+  for (;; ++sh.entry) {  // entries without rows have no steps
+    x.seq = sh.entry / row_tiles;
+    x.r = item_range(p, x.seq, sh.entry % row_tiles);
+    cost = x.r.cost();
+    if (at < first + (long long)cost * heads) break;
+    first += (long long)cost * heads;
+  }
+  sh.first = first;
+  x.kh = (int)((at - first) / cost);
+  const long long p0 = first + (long long)x.kh * cost, p1 = p0 + cost;
+  const long long to = min(sh.cut[1], p1);
+  item_parts(sh, p0, p1, at, x);
+  if (x.r.begin < x.r.end) {
+    const int from = at == p0 ? x.r.begin : x.r.begin + (int)(at - p0) - kItemCost;
+    const int until = x.r.begin + (int)(to - p0) - kItemCost;
+    x.r.begin = from, x.r.end = until;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) x.r.lo[t] = max(x.r.lo[t], from), x.r.hi[t] = min(x.r.hi[t], until);
+  }
+  sh.cut[0] = to;
+  out = x;
+}
+
+// A warp's 32 query rows of a segment to the shared-memory tile, D/16 lanes (32 bytes each) per row,
+// all loads in flight at once. The row's largest value moves to [2^12, 2^13): exact in float16 down
+// to 2^-36 of it. The sign of the score's factor goes into the query, so that maxima stay maxima.
 template <int D, bool MX>
-__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_constant__ AttnParams p) {
+__device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w, int t, int row_base, int lane, uint32_t q_tile,
+                                             float *coef) {
+  constexpr int L = D / 16, RW = 32 / L, N = 32 / RW;
+  const int sub = lane / L, chunk = lane % L * 2;
+  const float factor = (MX || !p.c.k_scale ? 1.f : __ldg(p.c.k_scale + w.kh)) * p.scale_log2;
+  uint4 v[N][2];
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    const int r = t * kRows + row_base + x * RW + sub, row = w.r.row0 + r;
+    const int at = token_of(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
+    v[x][0] = v[x][1] = make_uint4(0, 0, 0, 0);
+    if (r < w.r.rows && token >= 0 && token < p.b.tokens) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)token * p.q_stride + head * D) + chunk;
+      v[x][0] = __ldg(src), v[x][1] = __ldg(src + 1);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    float am = 0.f;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      am = max3abs(max3abs(am, bf16lo(v[x][y].x), bf16hi(v[x][y].x)), bf16lo(v[x][y].y), bf16hi(v[x][y].y));
+      am = max3abs(max3abs(am, bf16lo(v[x][y].z), bf16hi(v[x][y].z)), bf16lo(v[x][y].w), bf16hi(v[x][y].w));
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+    const int e = max((int)(__float_as_uint(am) >> 23) - 127, -100);
+    const float up = copysignf(__uint_as_float((uint32_t)(127 + 12 - e) << 23), factor);
+    const int r = row_base + x * RW + sub;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      sts128(tile_addr(q_tile, r, chunk + y), kv_pack_half2(bf16lo(v[x][y].x) * up, bf16hi(v[x][y].x) * up),
+             kv_pack_half2(bf16lo(v[x][y].y) * up, bf16hi(v[x][y].y) * up),
+             kv_pack_half2(bf16lo(v[x][y].z) * up, bf16hi(v[x][y].z) * up),
+             kv_pack_half2(bf16lo(v[x][y].w) * up, bf16hi(v[x][y].w) * up));
+    const float c = __uint_as_float((uint32_t)(127 - 12 + e) << 23) * fabsf(factor);
+    if (chunk == 0) coef[r] = c < 1e-37f ? 1e-37f : c;  // 0 must not meet the masked -inf
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
+template <int D, bool MX>
+__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_constant__ AttnParams p, int row_tiles) {
   using M = TileSmem<D>;
   constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
+  __shared__ Share share;
+  __shared__ Work ring[2];
+  __shared__ long long warp_sums[kThreads / 32];
+  __shared__ float row_coef[2 * kRows];  // score factor of each row of the segment
   __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t last_part[2];
   __shared__ volatile uint32_t abort_flag;
   __shared__ volatile uint32_t valid[kValidRing];  // a byte per dequantizing warp: two groups' bits
 
-  const Work w = block_work(p);
-  if (w.rows <= 0) return;
   const uint32_t base = (kv_smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
   const uint64_t limit = p.limit_ns;
   auto bar = [&](const uint64_t &b) { return kv_smem_u32(&b); };
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bars.q_full[i]), kRows);
-      mbar_init(bar(bars.k_full[i]), 128);
-      mbar_init(bar(bars.v_full[i]), 128);
-      mbar_init(bar(bars.k_empty[i]), 1);
-      mbar_init(bar(bars.v_empty[i]), 1);
-      mbar_init(bar(bars.s_full[i]), 1);
-      mbar_init(bar(bars.p_full[i]), kRows);
-      mbar_init(bar(bars.o_full[i]), 1);
+      mbar_init(bar(bars.work_full[i]), 1);
+      mbar_init(bar(bars.work_empty[i]), kWorkReaders);
+      mbar_init(bar(bars.q_full[i]), 4);
+      mbar_init(bar(bars.k_full[i]), 4);
+      mbar_init(bar(bars.v_full[i]), 4);
+      mbar_init(bar(bars.k_empty[i]), 2);
+      mbar_init(bar(bars.v_empty[i]), 2);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(bars.s_full[i][h]), 1);
+        mbar_init(bar(bars.p_full[i][h]), 4);
+        mbar_init(bar(bars.pv_done[i][h]), 1);
+      }
+      mbar_init(bar(bars.o_empty[i]), 4);
+      mbar_init(bar(bars.drain[i]), 1);
     }
-    mbar_init(bar(bars.drain), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  find_share(p, row_tiles, &share, warp_sums);
+  if (share.cut[0] >= share.cut[1]) return;
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem_u32(&tmem_slot)), "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -333,233 +585,359 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_slot, 0);  // uniform
 
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int t = warp >> 2, r = threadIdx.x & 127;
-    const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
-    const int row = w.row0 + t * kRows + r;  // row of the sequence's key head
-    const bool live = t * kRows + r < w.rows;
-    const int token = w.q0 + row / p.group, head = w.kh * p.group + row % p.group;
-    const bool real = live && token >= 0 && token < p.b.tokens;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 tensor-memory lanes
     const uint32_t s_tm = tmem + lanes + t * 128, o_tm = tmem + lanes + 256 + t * 128;
-    bool ok = true;
-    float c;
-    {
-      // the row's largest value moves to [2^12, 2^13): exact in float16 down to 2^-36 of it
-      uint32_t raw[D / 2];
-      float am = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (real) v = __ldg(reinterpret_cast<const uint4 *>(p.q + (size_t)token * p.q_stride + head * D) + i);
-        raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
-      }
-#pragma unroll
-      for (int i = 0; i < D / 2; ++i) am = max3abs(am, bf16lo(raw[i]), bf16hi(raw[i]));
-      const int e = max((int)(__float_as_uint(am) >> 23) - 127, -100);
-      const float factor = (MX || !p.c.k_scale ? 1.f : __ldg(p.c.k_scale + w.kh)) * p.scale_log2;
-      // the sign of the score's factor goes into the query, so that maxima stay maxima
-      const float up = copysignf(__uint_as_float((uint32_t)(127 + 12 - e) << 23), factor);
-      c = __uint_as_float((uint32_t)(127 - 12 + e) << 23) * fabsf(factor);
-      if (c < 1e-37f) c = 1e-37f;  // a factor of zero must not meet the masked -inf
-      const uint32_t q_tile = base + M::kQ + t * M::kTile;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        uint32_t h[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) h[x] = kv_pack_half2(bf16lo(raw[4 * i + x]) * up, bf16hi(raw[4 * i + x]) * up);
-        sts128(tile_addr(q_tile, r, i), h[0], h[1], h[2], h[3]);
-      }
-      fence_proxy_async();
-      mbar_arrive(bar(bars.q_full[t]));
-    }
-    const int pos = w.first_pos + row / p.group;
-    const int see_hi = p.causal ? min(pos, w.kv_len - 1) : w.kv_len - 1;
-    const int see_lo = p.causal && p.window > 0 ? pos - p.window : -1;
-    const int last = min(w.rows, (t + 1) * kRows) - 1;
-    const int tile_lo = w.first_pos + (w.row0 + t * kRows) / p.group, tile_hi = w.first_pos + (w.row0 + max(last, 0)) / p.group;
-    float m = -INFINITY, l = 0.f;  // m: reference of the exponentials, in units of log2
-    for (int i = lo; i < hi; ++i) {
-      const int it = i - lo;
-      if (!(ok = mbar_wait_warp(bar(bars.s_full[t]), it & 1, limit, &abort_flag))) break;
-      tc_fence_after();
-      uint32_t sr[128];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) tm_ld32(s_tm + 32 * x, sr + 32 * x);
-      tc_wait_ld();
-      float *s = reinterpret_cast<float *>(sr);
-      const int key0 = i * kKeys;
-      const uint32_t groups = valid[(i - w.begin) % kValidRing];
-      const bool whole = groups == 0x03030303u && key0 + kKeys <= w.kv_len &&
-                         (!p.causal || (key0 + kKeys - 1 <= tile_lo && (p.window <= 0 || key0 > tile_hi - p.window)));
-      if (!whole) {
-        const int top = see_hi - key0, bottom = see_lo - key0;
-#pragma unroll
-        for (int j = 0; j < 128; ++j)
-          if (j > top || j <= bottom || !((groups >> (8 * (j / 32) + (j / 16) % 2)) & 1u)) s[j] = -INFINITY;
-      }
-      float mx = -INFINITY, mx2 = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 128; j += 4) mx = max3(mx, s[j], s[j + 1]), mx2 = max3(mx2, s[j + 2], s[j + 3]);
-      const float top = fmaxf(mx, mx2) * c;
-      const bool grew = top > m + 8.f || (m == -INFINITY && top > m);
-      if (__any_sync(0xFFFFFFFFu, grew)) {
-        const float next = grew ? top : m;
-        const float f = grew ? kv_ex2(m - next) : 1.f;  // 0 where nothing was seen before
-        m = next;
-        l *= f;
-        if (it > 0) {  // the scores' arrival says that the products before them are done
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t ov[32];
-            tm_ld32(o_tm + 32 * x, ov);
-            tc_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * f);
-            tm_st32(o_tm + 32 * x, ov);
+    int n = 0, steps = 0;  // steps of this row tile, key steps of all segments so far
+    auto queries = [&](int seg) {
+      const Work &x = ring[seg & 1];
+      if ((t ? x.r.lo[1] : x.r.lo[0]) >= (t ? x.r.hi[1] : x.r.hi[0])) return;
+      load_queries<D, MX>(p, x, t, 32 * (warp & 3), lane, base + M::kQ + t * M::kTile, row_coef + t * kRows);
+      mbar_arrive_warp(bar(bars.q_full[t]));
+    };
+    bool more = get_work(bars, ring, 0, limit, &abort_flag);
+    if (more) queries(0);
+    for (int seg = 0; more; done_work(bars, seg), ++seg) {
+      const Work &w = ring[seg & 1];
+      const int lo = t ? w.r.lo[1] : w.r.lo[0], hi = t ? w.r.hi[1] : w.r.hi[0];
+      const int step0 = steps - w.r.begin;
+      steps += w.r.end - w.r.begin;
+      const int kv_len = w.r.kv_len, pos = w.r.first_pos + token_of(p, w.r.row0 + t * kRows + r);
+      const int see_hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
+      const int see_lo = p.causal && p.window > 0 ? pos - p.window : -1;
+      const int last = max(min(w.r.rows, (t + 1) * kRows) - 1, 0);
+      const int tile_lo = w.r.first_pos + token_of(p, w.r.row0 + t * kRows), tile_hi = w.r.first_pos + token_of(p, w.r.row0 + last);
+      const float c = row_coef[t * kRows + r];  // of this warp's making; unused without steps
+      float m = -INFINITY, l = 0.f;  // m: reference of the exponentials, in units of log2
+      bool ok = true;
+      for (int i = lo; i < hi && ok; ++i, ++n) {
+        const int key0 = i * kKeys;
+        uint32_t groups = 0x03030303u;
+        bool whole = true;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!(ok = mbar_wait_warp(bar(bars.s_full[t][h]), n & 1, limit, &abort_flag))) break;
+          tc_fence_after();
+          uint32_t sr[64];
+          tm_ld32(s_tm + 64 * h, sr), tm_ld32(s_tm + 64 * h + 32, sr + 32);
+          if (h == 0) {
+            groups = valid[(step0 + i) % kValidRing];
+            whole = groups == 0x03030303u && key0 + kKeys <= kv_len &&
+                    (!p.causal || (key0 + kKeys - 1 <= tile_lo && (p.window <= 0 || key0 > tile_hi - p.window)));
           }
+          tc_wait_ld();
+          float *s = reinterpret_cast<float *>(sr);
+          if (!whole) {
+            const int top = see_hi - key0 - 64 * h, bottom = see_lo - key0 - 64 * h;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t g = groups >> (16 * h + 8 * x);
+              const uint32_t there = (g & 1u ? 0xFFFFu : 0u) | (g & 2u ? 0xFFFF0000u : 0u);
+              const uint32_t see = there & bits_below(top + 1 - 32 * x) & ~bits_below(bottom + 1 - 32 * x);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[32 * x + j] = see & (1u << j) ? s[32 * x + j] : -INFINITY;
+            }
+          }
+          // The exponentials are formed against the reference at hand while the maximum is taken, and
+          // once more in the rare half whose maximum is too far above it.
+          const uint64_t c2 = pack2(c, c);
+          uint32_t pr[32];
+          float sum;
+          auto exponentials = [&]() {
+            const float shift = m == -INFINITY ? 0.f : -m;
+            const uint64_t shift2 = pack2(shift, shift);
+            uint64_t sums[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float a, b;
+              unpack2(fma2(pack2(s[2 * j], s[2 * j + 1]), c2, shift2), a, b);
+              a = kv_ex2(a), b = kv_ex2(b);
+              sums[j & 1] = add2(sums[j & 1], pack2(a, b));
+              pr[j] = kv_pack_half2(a, b);
+            }
+            float a, b;
+            unpack2(add2(sums[0], sums[1]), a, b);
+            sum = a + b;
+          };
+          exponentials();
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 64; j += 8)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[j + 2 * x], s[j + 2 * x + 1]);
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+          const bool grew = top > m + 8.f;
+          if (__any_sync(0xFFFFFFFFu, grew)) {
+            const float next = grew ? top : m;
+            const float f = grew ? kv_ex2(m - next) : 1.f;  // 0 where nothing was seen before
+            m = next;
+            l *= f;
+            exponentials();
+            if (i > lo || h > 0) {
+              // the products of the half before must be in O
+              if (!(ok = mbar_wait_warp(bar(bars.pv_done[t][h ^ 1]), (h ? n : n - 1) & 1, limit, &abort_flag))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int x = 0; x < D / 32; ++x) {
+                uint32_t ov[32];
+                tm_ld32(o_tm + 32 * x, ov);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * f);
+                tm_st32(o_tm + 32 * x, ov);
+              }
+            }
+          }
+          tm_st32(s_tm + 64 * h, pr);
+          l += sum;
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive_warp(bar(bars.p_full[t][h]));
         }
       }
-      const float shift = m == -INFINITY ? 0.f : -m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pr[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float a = kv_ex2(fmaf(s[64 * half + 2 * j], c, shift)), b = kv_ex2(fmaf(s[64 * half + 2 * j + 1], c, shift));
-          sum[(2 * j) & 3] += a, sum[(2 * j + 1) & 3] += b;
-          pr[j] = kv_pack_half2(a, b);
-        }
-        tm_st32(s_tm + 32 * half, pr);
+      if (!ok) break;
+      if (m == INFINITY) l = NAN;  // an infinite score has no softmax
+      // every score product of this segment has arrived: its queries may go
+      more = get_work(bars, ring, seg + 1, limit, &abort_flag);
+      if (more) queries(seg + 1);
+      if (t * kRows >= w.r.rows) continue;
+      const bool any = lo < hi;
+      if (any) {
+        if (!mbar_wait_warp(bar(bars.pv_done[t][1]), (n - 1) & 1, limit, &abort_flag)) break;
+        tc_fence_after();
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(bars.p_full[t]));
-    }
-    const bool any = lo < hi;
-    if (any && ok) ok = mbar_wait_warp(bar(bars.o_full[t]), 0, limit, &abort_flag);
-    tc_fence_after();
-    if (ok && __any_sync(0xFFFFFFFFu, real)) {
-      const float inv = l == 0.f ? 0.f : (MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + w.kh)) / l;
+      const int row = w.r.row0 + t * kRows + r;  // row of the sequence's key head
+      const bool live = t * kRows + r < w.r.rows;
+      const int at = token_of(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
+      const bool real = live && token >= 0 && token < p.b.tokens;
+      const float v_scale = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + w.kh);
       uint16_t *dst = p.y + ((size_t)token * p.q_heads + head) * D;
+      auto put = [&](int x, const float *o, float f) {  // 32 elements of the row
+        uint32_t out[16];
 #pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * j] * f, o[2 * j + 1] * f);
+          out[j] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        if (real) st256(dst + 32 * x, out), st256(dst + 32 * x + 16, out + 8);
+      };
+      auto put_lse = [&](float mm, float ll) {
+        if (real && p.lse)
+          p.lse[(size_t)token * p.q_heads + head] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * 0.69314718055994531f;
+      };
+      const float inv = l == 0.f ? 0.f : v_scale / l;
+      // parts: [block][first or not][row tile]: O by column, then m and l
+      const int tiles = p.b.max_q * p.group > kRows ? 2 : 1;
+      float *const parts = reinterpret_cast<float *>(p.workspace + kAttnCounterBytes);
+      auto part_at = [&](int j) {
+        return parts + (((size_t)(w.owner + j) * 2 + (j == 0 ? 1 : 0)) * tiles + t) * kRows * (D + 2) + r;
+      };
+      float *mine = part_at(w.part);
+#pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t ov[32];
         if (any) {
           tm_ld32(o_tm + 32 * x, ov);
           tc_wait_ld();
-        }
-        uint32_t out[16];
+        } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float a = any ? __uint_as_float(ov[2 * j]) * inv : 0.f, b = any ? __uint_as_float(ov[2 * j + 1]) * inv : 0.f;
-          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-          out[j] = *reinterpret_cast<const uint32_t *>(&h);
+          for (int j = 0; j < 32; ++j) ov[j] = 0u;
         }
-        if (real) {
+        const float *o = reinterpret_cast<const float *>(ov);
+        if (w.parts == 1) put(x, o, inv);
+        else if (live) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            reinterpret_cast<uint4 *>(dst + 32 * x)[j] = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+          for (int j = 0; j < 32; ++j) __stcg(mine + (32 * x + j) * kRows, o[j]);
         }
       }
-      if (real && p.lse)
-        p.lse[(size_t)token * p.q_heads + head] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+      if (any) {
+        tc_fence_before();
+        mbar_arrive_warp(bar(bars.o_empty[t]));
+      }
+      if (w.parts == 1) {
+        put_lse(m, l);
+        continue;
+      }
+      if (live) __stcg(mine + D * kRows, m), __stcg(mine + (D + 1) * kRows, l);
+      __threadfence();
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+      if (r == 0) {
+        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + 2 * w.owner + t;
+        const uint32_t before = atomicAdd(counter, 1u);
+        last_part[t] = before + 1 == (uint32_t)w.parts;
+        if (last_part[t]) *counter = 0;  // ready for the next call
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+      if (!last_part[t]) continue;
+      __threadfence();
+      if (!live) continue;
+      float mm = -INFINITY, ll = 0.f;
+      for (int j = 0; j < w.parts; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      for (int j = 0; j < w.parts; ++j)
+        ll += __ldcg(part_at(j) + (D + 1) * kRows) * kv_ex2(__ldcg(part_at(j) + D * kRows) - ref);
+      const float inv_all = ll == 0.f ? 0.f : v_scale / ll;
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        float o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+        for (int j = 0; j < w.parts; ++j) {
+          const float *src = part_at(j);
+          const float f = kv_ex2(__ldcg(src + D * kRows) - ref);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(src + (32 * x + e) * kRows), f, o[e]);
+        }
+        put(x, o, inv_all);
+      }
+      put_lse(mm, ll);
     }
     tc_fence_before();
   } else if (warp < 12) {
     // ------------------------------------------------------------------ codes to float16
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    const int dw = warp - 8, seq_row = (blockIdx.x % (p.b.n_seq * p.c.kv_heads)) / p.c.kv_heads;
-    const int *table = p.b.page_table + (size_t)seq_row * p.b.max_pages;
-    const int group_mask = (1 << (p.c.page_shift - 4)) - 1;
-    auto page_of = [&](int i, int g) -> int {  // page id of the warp's group g of step i; -1: no keys there
-      const int gi = i * 8 + 2 * dw + g, col = gi >> (p.c.page_shift - 4);
-      if (i >= w.end || 16 * gi >= w.kv_len || col >= p.b.max_pages) return -1;
-      const int page = __ldg(table + col);
-      return page < p.c.num_pages ? page : -1;
-    };
-    auto place = [&](int i, int g, int page) -> const uint8_t * {
-      if (page < 0) return nullptr;
-      const int gi = i * 8 + 2 * dw + g;
-      return p.c.pages + ((((size_t)page * p.c.kv_heads + w.kh) << (p.c.page_shift - 4)) + (gi & group_mask)) * G.bytes;
-    };
-    Codes<D, MX> ck, cv;
-    int next0 = page_of(w.begin, 0), next1 = page_of(w.begin, 1);
-    const uint8_t *grp[2] = {place(w.begin, 0, next0), place(w.begin, 1, next1)};
-    if (w.begin < w.end) {
-      load_k<D, MX>(grp, lane, ck);
-      load_v<D, MX>(grp, lane, cv);
-    }
-    next0 = page_of(w.begin + 1, 0), next1 = page_of(w.begin + 1, 1);
-    for (int i = w.begin; i < w.end; ++i) {
-      const int it = i - w.begin, st = it & 1;
-      const uint32_t bits = (grp[0] ? 1u : 0u) | (grp[1] ? 2u : 0u);
-      grp[0] = place(i + 1, 0, next0), grp[1] = place(i + 1, 1, next1);
-      next0 = page_of(i + 2, 0), next1 = page_of(i + 2, 1);
-      if (it >= 2 && !mbar_wait(bar(bars.k_empty[st]), ((it >> 1) - 1) & 1, limit, &abort_flag)) break;
-      store_k<D, MX>(base + M::kK + st * M::kTile, 32 * dw, lane, ck);
-      if (lane == 0) reinterpret_cast<volatile uint8_t *>(&valid[it % kValidRing])[dw] = (uint8_t)bits;
-      fence_proxy_async();
-      mbar_arrive(bar(bars.k_full[st]));
-      load_k<D, MX>(grp, lane, ck);
-      if (it >= 2 && !mbar_wait(bar(bars.v_empty[st]), ((it >> 1) - 1) & 1, limit, &abort_flag)) break;
-      store_v<D, MX>(base + M::kV + st * M::kTile, 32 * dw, lane, w.kv_len - (i * kKeys + 32 * dw), cv);
-      fence_proxy_async();
-      mbar_arrive(bar(bars.v_full[st]));
-      load_v<D, MX>(grp, lane, cv);
-    }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12 && lane == 0) {
-      // ---------------------------------------------------------------- MMA issue
-      constexpr uint32_t id_s = idesc_f16(kKeys, false), id_o = idesc_f16(D, true);
-      bool ok = true;
-      auto scores = [&](int t, int st) {
-        const uint32_t qa = base + M::kQ + t * M::kTile, ka = base + M::kK + st * M::kTile;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * M::kSlab + (k & 3) * 32;
-          mma_ss(tmem + t * 128, desc(kDescK, qa + off), desc(kDescK, ka + off), id_s, k > 0);
-        }
-        tc_commit(bar(bars.s_full[t]));
+    const int dw = warp - 8, group_mask = (1 << (p.c.page_shift - 4)) - 1;
+    int n = 0;  // key steps of all segments
+    bool ok = true;
+    for (int seg = 0; ok && get_work(bars, ring, seg, limit, &abort_flag); ++seg) {
+      const int begin = ring[seg & 1].r.begin, end = ring[seg & 1].r.end, kv_len = ring[seg & 1].r.kv_len, kh = ring[seg & 1].kh;
+      const int *table = p.b.page_table + (size_t)ring[seg & 1].seq * p.b.max_pages;
+      done_work(bars, seg);
+      auto page_of = [&](int i, int g) -> int {  // page id of the warp's group g of step i; -1: no keys there
+        const int gi = i * 8 + 2 * dw + g, col = gi >> (p.c.page_shift - 4);
+        if (i >= end || 16 * gi >= kv_len || col >= p.b.max_pages) return -1;
+        const int page = __ldg(table + col);
+        return page < p.c.num_pages ? page : -1;
       };
-      for (int i = w.begin - 1; ok && i < w.end; ++i) {
-        const int it = i - w.begin;
-        const bool more = i + 1 < w.end;
-        if (more && !(ok = mbar_wait(bar(bars.k_full[(it + 1) & 1]), ((it + 1) >> 1) & 1, limit, &abort_flag))) break;
-        if (it >= 0 && !(ok = mbar_wait(bar(bars.v_full[it & 1]), (it >> 1) & 1, limit, &abort_flag))) break;
-        tc_fence_after();
+      auto place = [&](int i, int g, int page) -> const uint8_t * {
+        if (page < 0) return nullptr;
+        const int gi = i * 8 + 2 * dw + g;
+        return p.c.pages + ((((size_t)page * p.c.kv_heads + kh) << (p.c.page_shift - 4)) + (gi & group_mask)) * G.bytes;
+      };
+      // K runs one step ahead of V, as the products do
+      Codes<D, MX> ck, cv;
+      int next0 = page_of(begin, 0), next1 = page_of(begin, 1);
+      const uint8_t *k_grp[2] = {place(begin, 0, next0), place(begin, 1, next1)};
+      load_k<D, MX>(k_grp, lane, ck);
+      load_v<D, MX>(k_grp, lane, cv);
+      next0 = page_of(begin + 1, 0), next1 = page_of(begin + 1, 1);
+      for (int i = begin - 1; i < end; ++i) {
+        if (i + 1 < end) {
+          const int nk = n + 1 + i - begin, st = nk & 1;
+          const uint32_t bits = (k_grp[0] ? 1u : 0u) | (k_grp[1] ? 2u : 0u);
+          if (nk >= 2 && !(ok = mbar_wait(bar(bars.k_empty[st]), ((nk >> 1) - 1) & 1, limit, &abort_flag))) break;
+          store_k<D, MX>(base + M::kK + st * M::kTile, 32 * dw, lane, ck);
+          if (lane == 0) reinterpret_cast<volatile uint8_t *>(&valid[nk % kValidRing])[dw] = (uint8_t)bits;
+          fence_proxy_async();
+          mbar_arrive_warp(bar(bars.k_full[st]));
+        }
+        const uint8_t *v_grp[2] = {k_grp[0], k_grp[1]};
+        k_grp[0] = place(i + 2, 0, next0), k_grp[1] = place(i + 2, 1, next1);
+        next0 = page_of(i + 3, 0), next1 = page_of(i + 3, 1);
+        load_k<D, MX>(k_grp, lane, ck);
+        if (i < begin) continue;
+        const int nv = n + i - begin, st = nv & 1;
+        if (nv >= 2 && !(ok = mbar_wait(bar(bars.v_empty[st]), ((nv >> 1) - 1) & 1, limit, &abort_flag))) break;
+        store_v<D, MX>(base + M::kV + st * M::kTile, 32 * dw, lane, kv_len - (i * kKeys + 32 * dw), cv);
+        fence_proxy_async();
+        mbar_arrive_warp(bar(bars.v_full[st]));
+        load_v<D, MX>(v_grp, lane, cv);
+      }
+      n += end - begin;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+  } else if (warp < 14) {
+    // ------------------------------------------------------------------ MMA issue
+    // One warp per row tile: a single one, waiting for one tile's operands and then the other's, left
+    // the tensor pipe idle a third of the time. The whole warp takes every step, so that the elected
+    // thread's operands stay uniform.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    constexpr uint32_t id_s = idesc_f16(kKeys / 2, false), id_o = idesc_f16(D, true);
+    const int t = warp - 12;
+    const bool lead = elect_one();
+    bool ok = true;
+    auto wait = [&](const uint64_t &b, uint32_t parity) {
+      ok = ok && mbar_wait_warp(bar(b), parity, limit, &abort_flag);
+      tc_fence_after();
+    };
+    const uint32_t qd = desc_low(16, base + M::kQ + t * M::kTile), o_tm = tmem + 256 + t * 128, s_tm = tmem + t * 128;
+    uint32_t q_n = 0, p_n = 0, items = 0;  // parities of the queries and of the products; there was an item
+    int n0 = 0;                            // key steps of all segments
+    for (int seg = 0; ok && get_work(bars, ring, seg, limit, &abort_flag); ++seg) {
+      const Range &r = ring[seg & 1].r;
+      auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+      const int begin = uniform(r.begin), end = uniform(r.end), lo = uniform(t ? r.lo[1] : r.lo[0]), hi = uniform(t ? r.hi[1] : r.hi[0]);
+      done_work(bars, seg);
+      for (int i = begin - 1; ok && i < end; ++i) {
+        const int n = n0 + i - begin;
+        const bool more = i + 1 < end, products = i >= lo && i < hi, scores = i + 1 >= lo && i + 1 < hi;
+        // a tile without keys here waits too: both warps hand every operand tile back, once a step
+        if (more) wait(bars.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+        if (i >= begin) wait(bars.v_full[n & 1], (n >> 1) & 1);
+        const uint32_t vd = desc_low(16384, base + M::kV + (n & 1) * M::kTile);
+        const uint32_t kd = desc_low(16, base + M::kK + ((n + 1) & 1) * M::kTile);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok) break;
-          if (i >= w.lo[t] && i < w.hi[t]) {
-            if (!(ok = mbar_wait(bar(bars.p_full[t]), (i - w.lo[t]) & 1, limit, &abort_flag))) break;
-            tc_fence_after();
-            const uint32_t va = base + M::kV + (it & 1) * M::kTile;
+        for (int h = 0; h < 2; ++h) {
+          if (products) {
+            // O is written anew with the first product: the segment before must have read it
+            if (h == 0 && i == lo && items) wait(bars.o_empty[t], q_n);
+            wait(bars.p_full[t][h], p_n);
+            if (ok && lead) {
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k, desc(kDescV, va + k * 2048), id_o, k > 0 || i > w.lo[t]);
-            if (i == w.hi[t] - 1) tc_commit(bar(bars.o_full[t]));
+              for (int k = 0; k < 4; ++k)
+                mma_ts(o_tm, s_tm + 64 * h + 8 * k, vd + h * 512 + k * 128, id_o, k > 0 || h > 0 || i > lo);
+              tc_commit(bar(bars.pv_done[t][h]));
+            }
+            __syncwarp();
           }
-          if (i + 1 >= w.lo[t] && i + 1 < w.hi[t]) {
-            if (i + 1 == w.lo[t] && !(ok = mbar_wait(bar(bars.q_full[t]), 0, limit, &abort_flag))) break;
-            tc_fence_after();
-            scores(t, (it + 1) & 1);
+          if (scores) {
+            if (h == 0 && i + 1 == lo) {
+              wait(bars.q_full[t], q_n);
+              q_n ^= 1;
+            }
+            if (ok && lead) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k >> 2) * M::kSlab + (k & 3) * 32) >> 4;
+                mma_ss(s_tm + 64 * h, qd + off, kd + h * 512 + off, id_s, k > 0);
+              }
+              tc_commit(bar(bars.s_full[t][h]));
+            }
+            __syncwarp();
           }
         }
-        if (it >= 0) tc_commit(bar(bars.v_empty[it & 1]));
-        if (more) tc_commit(bar(bars.k_empty[(it + 1) & 1]));
+        if (products) p_n ^= 1, items |= i == hi - 1;
+        if (lead) {
+          if (i >= begin) tc_commit(bar(bars.v_empty[n & 1]));
+          if (more) tc_commit(bar(bars.k_empty[(n + 1) & 1]));
+        }
+        __syncwarp();
       }
-      // everything issued has finished before tensor memory and shared memory go
-      tc_commit(bar(bars.drain));
+      n0 += end - begin;
+    }
+    // everything issued has finished before tensor memory and shared memory go
+    if (lead) {
+      tc_commit(bar(bars.drain[t]));
       volatile uint32_t never = 0;
-      mbar_wait(bar(bars.drain), 0, kDrainLimitNs, &never);
+      mbar_wait(bar(bars.drain[t]), 0, kDrainLimitNs, &never);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ work list
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 14 && lane == 0) {
+      for (int seg = 0;; ++seg) {
+        if (seg >= 2 && !mbar_wait(bar(bars.work_empty[seg & 1]), ((seg >> 1) - 1) & 1, limit, &abort_flag)) break;
+        next_segment(p, row_tiles, share, ring[seg & 1]);
+        const bool end = ring[seg & 1].r.rows <= 0;
+        mbar_arrive(bar(bars.work_full[seg & 1]));
+        if (end) break;
+      }
     }
     __syncwarp();
   }
@@ -570,19 +948,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
   }
 }
 
+int row_tiles(const AttnParams &p) {
+  return (int)(((long long)p.b.max_q * p.group + 2 * kRows - 1) / (2 * kRows));
+}
+
 template <int D, bool MX>
 cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
   auto kernel = attn_tiles_kernel<D, MX>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<D>::kTotal);
   if (e != cudaSuccess) return e;
-  const long long row_tiles = ((long long)p.b.max_q * p.group + 2 * kRows - 1) / (2 * kRows);
-  const long long blocks = row_tiles * p.c.kv_heads * p.b.n_seq;
-  if (blocks > 0x7FFFFFFFll || (long long)p.b.max_q * p.group > 0x7FFF0000ll) return cudaErrorInvalidConfiguration;
-  kernel<<<(unsigned)blocks, kThreads, TileSmem<D>::kTotal, st>>>(p);
+  kernel<<<sm_count(), kThreads, TileSmem<D>::kTotal, st>>>(p, row_tiles(p));
   return cudaGetLastError();
 }
 
 }  // namespace
+
+size_t attention_tiles_workspace(const AttnParams &p, int d) {
+  const int tiles = (long long)p.b.max_q * p.group > kRows ? 2 : 1;  // row tiles that a part can have
+  return kAttnCounterBytes + (size_t)sm_count() * 2 * tiles * kRows * (d + 2) * sizeof(float);
+}
 
 cudaError_t launch_attention_tiles(const AttnParams &p, int d, int fmt, cudaStream_t st) {
   if (d == 128) return fmt ? launch_d<128, true>(p, st) : launch_d<128, false>(p, st);

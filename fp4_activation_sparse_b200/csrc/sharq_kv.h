@@ -76,6 +76,7 @@ struct AttnParams {
   float *lse;    // [tokens][q_heads] or null
   float scale_log2;  // softmax scale * log2(e)
   int q_heads, group;  // group = q_heads / kv_heads
+  uint32_t group_inv;  // ceil(2^32 / group): row / group = high word of row * group_inv, group > 1, row < 2^32 / group
   int causal, window;  // window 0: none
   uint8_t *workspace;
   unsigned long long limit_ns;  // of the bounded waits
@@ -93,6 +94,9 @@ struct NormResidualParams {
 cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t launch_kv_read(const ReadParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t st);
+// The attention workspace: counters (zero between calls), then parts of cut items.
+constexpr int kAttnCounterBytes = 8192;
+size_t attention_tiles_workspace(const AttnParams &p, int d);
 cudaError_t launch_attention_tiles(const AttnParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t read_and_clear_attn_status(uint32_t *status);
 size_t attention_workspace(const AttnParams &p, int d);

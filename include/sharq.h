@@ -362,7 +362,7 @@ int sharq_kv_read(const sharq_kv_cache *cache, const sharq_kv_batch *batch, void
                   int out_dtype, void *stream);
 
 /* Attention of the batch's queries over the cache. Query head h reads key head
- * h / (q_heads / kv_heads).
+ * h / (q_heads / kv_heads); max_q * (q_heads / kv_heads)^2 is below 2^32.
  *   q_bf16_dev    [tokens][q_heads][head_dim] bf16, rows q_stride elements apart (a multiple of 8)
  *   causal        token i sees the positions up to its own (the call's own keys must have been
  *                 appended), and with window > 0 only the last `window` of them; otherwise every
