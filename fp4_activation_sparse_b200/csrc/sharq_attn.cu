@@ -8,7 +8,15 @@
 // scales and the softmax scale are applied in float32. Queries are scaled by a power of two per
 // row and are exact in float16 too. Probabilities are rounded to float16 (11 bits, against the
 // 8 of the bfloat16 output); their sum, the maxima and both accumulators are float32.
+//
+// Bound by the cache's bytes (144 or 136 per key and key head at 128 elements). Every block takes an
+// equal, contiguous share of all key steps of the launch, found from the device's own lengths, so
+// that ragged batches balance and a few long sequences fill the GPU; its eight warps walk a
+// segment's 32-key tiles in turn, each with copies of its own in flight, and join at its end. The
+// parts of an item that is cut between blocks go through the workspace; the block that arrives last
+// joins them in the order of the keys.
 #include "sharq_common.cuh"
+#include "sharq_internal.h"
 #include "sharq_kv.h"
 #include "sharq_kv_device.cuh"
 
@@ -18,6 +26,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTile = 32;   // keys per step of a warp: two groups of the cache
 constexpr int kStagesA = 3;  // tiles in flight per warp
+constexpr int kItemCost = 8;  // what an item costs besides its tiles (queries, joining eight warps), in tiles
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -80,6 +89,29 @@ struct RowsKernel {
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
 };
 
+// One sequence's query rows (all of them: the launch has at most R per key head) and key tiles.
+struct RowsRange {
+  int q0, rows, kv_len, first_pos, lo, hi;
+  __device__ __forceinline__ int cost() const { return rows <= 0 ? 0 : kItemCost + max(1, hi - lo); }
+};
+__device__ __forceinline__ RowsRange rows_range(const AttnParams &p, int seq) {
+  RowsRange r;
+  const int q1 = __ldg(p.b.cu_q + seq + 1);
+  r.q0 = __ldg(p.b.cu_q + seq);
+  r.kv_len = __ldg(p.b.kv_len + seq);
+  const int q_len = min(q1 - r.q0, p.b.max_q);
+  r.rows = q_len * p.group;
+  r.first_pos = r.kv_len - (q1 - r.q0);  // position of the sequence's first new token
+  int k_lo = 0, k_hi = min(r.kv_len, p.b.max_pages << p.c.page_shift);  // no place behind the table
+  if (p.causal) {
+    k_hi = min(k_hi, r.first_pos + q_len);
+    if (p.window > 0) k_lo = max(0, r.first_pos - p.window + 1);
+  }
+  r.lo = k_lo / kTile;
+  r.hi = (max(k_hi, 0) + kTile - 1) / kTile;
+  return r;
+}
+
 template <int D, bool MX, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel(const AttnParams p) {
   using C = RowsKernel<D, MX, NT>;
@@ -87,26 +119,34 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
   constexpr int KS = C::KS;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float sh_m[kWarps][C::R], sh_l[kWarps][C::R];
+  __shared__ Share share;
+  __shared__ long long warp_sums[kWarps];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int row_tiles = (p.b.max_q * p.group + C::R - 1) / C::R;
-  int w = blockIdx.x;
-  const int rt = w % row_tiles;
-  w /= row_tiles;
-  const int kh = w % p.c.kv_heads, seq = w / p.c.kv_heads;
-
-  const int q0 = __ldg(p.b.cu_q + seq), q_len = min(__ldg(p.b.cu_q + seq + 1) - q0, p.b.max_q);
-  const int kv_len = __ldg(p.b.kv_len + seq);
-  const int rows = min(q_len * p.group - rt * C::R, C::R);
-  if (rows <= 0) return;
-  const int first_pos = kv_len - (__ldg(p.b.cu_q + seq + 1) - q0);  // position of the sequence's first new token
-  const int pos_lo = first_pos + rt * C::R / p.group, pos_hi = first_pos + (rt * C::R + rows - 1) / p.group;
-  int k_lo = 0, k_hi = min(kv_len, p.b.max_pages << p.c.page_shift);  // no place behind the table
-  if (p.causal) {
-    k_hi = min(k_hi, pos_hi + 1);
-    if (p.window > 0) k_lo = max(0, pos_lo - p.window + 1);
+  find_share<kWarps * 32, kItemCost>(p.b.n_seq, p.c.kv_heads, kWarps, &share, warp_sums,
+                                     [&](long long e) { return rows_range(p, (int)e).cost(); });
+  int seq = share.entry;
+  long long first = share.first;
+  for (long long at = share.cut[0]; at < share.cut[1];) {
+  RowsRange w;
+  int cost;
+  for (;; ++seq) {  // sequences without new tokens have no items
+    w = rows_range(p, seq);
+    cost = w.cost();
+    if (at < first + (long long)cost * p.c.kv_heads) break;
+    first += (long long)cost * p.c.kv_heads;
   }
-  const int t_lo = k_lo / kTile, t_hi = (max(k_hi, 0) + kTile - 1) / kTile;
+  const int kh = (int)((at - first) / cost);
+  const long long p0 = first + (long long)kh * cost, p1 = p0 + cost, to = min(share.cut[1], p1);
+  const ItemParts parts = item_parts<kItemCost>(share, p0, p1, at);
+  int t_lo = w.lo, t_hi = w.hi;
+  if (t_lo < t_hi) {
+    t_hi = w.lo + (int)(to - p0) - kItemCost;
+    if (at != p0) t_lo = w.lo + (int)(at - p0) - kItemCost;
+  }
+  at = to;
+  const int q0 = w.q0, rows = w.rows, kv_len = w.kv_len, first_pos = w.first_pos;
+  const int pos_lo = first_pos, pos_hi = first_pos + token_of(p.group, p.group_inv, rows - 1);
 
   // ---- query fragments: lane (g, t) holds elements [D/4 * t, D/4 * (t + 1)) of row g of each n tile
   uint32_t qf[NT][KS][2];
@@ -114,8 +154,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
   const float ks = MX || !p.c.k_scale ? 1.f : __ldg(p.c.k_scale + kh);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = n * 8 + g, rr = rt * C::R + r;
-    const int token = q0 + rr / p.group, head = kh * p.group + rr % p.group;
+    const int r = n * 8 + g, tok = token_of(p.group, p.group_inv, r);
+    const int token = q0 + tok, head = kh * p.group + r - tok * p.group;
     uint32_t raw[KS * 2];
     if (r < rows && token >= 0 && token < p.b.tokens) {
       const uint16_t *src = p.q + (size_t)token * p.q_stride + head * D + t * (D / 4);
@@ -165,11 +205,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
     return page < p.c.num_pages ? page : -1;
   };
   // 16 tiles' page ids in the lanes: lane 2i + h has group h of the warp's tile base + i
-  int base = 0, ids = page_of(2 * (t_lo + warp + kWarps * (lane >> 1)) + (lane & 1));
+  auto page_ahead = [&](int i) { return page_of(2 * (t_lo + warp + kWarps * (i + (lane >> 1))) + (lane & 1)); };
+  int base = 0, ids = page_ahead(0), ids_next = page_ahead(16);
   auto tile_ids = [&](int i, int &a, int &b) {  // i-th tile of this warp (in increasing order of calls)
     if (i - base >= 16) {
       base += 16;
-      ids = page_of(2 * (t_lo + warp + kWarps * (base + (lane >> 1))) + (lane & 1));
+      ids = ids_next;
+      ids_next = page_ahead(base + 16);
     }
     a = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base));
     b = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base) + 1);
@@ -266,7 +308,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int pos = first_pos + (rt * C::R + n * 8 + 2 * t + c) / p.group;
+          const int pos = first_pos + token_of(p.group, p.group_inv, n * 8 + 2 * t + c);
           const int hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
           const int lo = p.causal && p.window > 0 ? pos - p.window : -1;
 #pragma unroll
@@ -409,14 +451,75 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
     }
     __syncthreads();
   }
-  if (warp != 0) return;
+  if (warp != 0) continue;  // the others begin the next segment
+  if (parts.count > 1) {
+    // parts: [block][first or not]: O in this lane order, then m and l by row
+    float *const all = reinterpret_cast<float *>(p.workspace + kAttnCounterBytes);
+    auto part_at = [&](int j) { return all + ((size_t)(parts.owner + j) * 2 + (j == 0 ? 1 : 0)) * C::R * (D + 2); };
+    float *mine = part_at(parts.index);
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) __stcg(mine + ((i * NT + n) * 4 + q) * 32 + lane, o[i][n][q]);
+    if (g == 0)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          __stcg(mine + C::R * D + 2 * (n * 8 + 2 * t + c), top[n][c]), __stcg(mine + C::R * D + 2 * (n * 8 + 2 * t + c) + 1, l[n][c]);
+    __threadfence();
+    __syncwarp();
+    uint32_t before = 0;
+    if (lane == 0) {
+      uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + parts.owner;
+      before = atomicAdd(counter, 1u);
+      if (before + 1 == (uint32_t)parts.count) *counter = 0;  // ready for the next call
+    }
+    if (__shfl_sync(0xFFFFFFFFu, before, 0) + 1 != (uint32_t)parts.count) continue;
+    __threadfence();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float mm = -INFINITY;
+        for (int j = 0; j < parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + C::R * D + 2 * (n * 8 + 2 * t + c)));
+        top[n][c] = mm;
+        l[n][c] = 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[i][n][q] = 0.f;
+    for (int j = 0; j < parts.count; ++j) {
+      const float *src = part_at(j);
+      float f[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float *ml = src + C::R * D + 2 * (n * 8 + 2 * t + c);
+          f[n][c] = kv_ex2(__ldcg(ml) - (top[n][c] == -INFINITY ? 0.f : top[n][c]));
+          l[n][c] += f[n][c] * __ldcg(ml + 1);
+        }
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[i][n][q] = fmaf(f[n][q & 1], __ldcg(src + ((i * NT + n) * 4 + q) * 32 + lane), o[i][n][q]);
+    }
+  }
   const float vs = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + kh);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int r = n * 8 + 2 * t + c, rr = rt * C::R + r;
-      const int token = q0 + rr / p.group, head = kh * p.group + rr % p.group;
+      const int r = n * 8 + 2 * t + c, tok = token_of(p.group, p.group_inv, r);
+      const int token = q0 + tok, head = kh * p.group + r - tok * p.group;
       if (r >= rows || token < 0 || token >= p.b.tokens) continue;
       const float inv = l[n][c] == 0.f ? 0.f : vs / l[n][c];  // a NaN query stays NaN
       // the lane's run of D/8 elements: rows g (even elements) and g + 8 (odd) of each 16-row tile
@@ -434,7 +537,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
         p.lse[(size_t)token * p.q_heads + head] =
             l[n][c] == 0.f ? -INFINITY : (top[n][c] + __log2f(l[n][c])) * 0.69314718055994531f;
     }
+  }
 }
+
+// tiles of 8 query rows: 1, 2 or 4; one of them leaves registers for two blocks per SM
+int row_tiles(const AttnParams &p) {
+  const long long rows = (long long)p.b.max_q * p.group;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+int blocks_of(int nt) { return sm_count() * (nt == 1 ? 2 : 1); }
 
 template <int D, bool MX, int NT>
 cudaError_t launch_rows(const AttnParams &p, cudaStream_t st) {
@@ -442,19 +553,14 @@ cudaError_t launch_rows(const AttnParams &p, cudaStream_t st) {
   auto kernel = attn_rows_kernel<D, MX, NT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const long long row_tiles = ((long long)p.b.max_q * p.group + C::R - 1) / C::R;
-  const long long blocks = row_tiles * p.c.kv_heads * p.b.n_seq;
-  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  kernel<<<(unsigned)blocks, kWarps * 32, C::kSmem, st>>>(p);
+  kernel<<<blocks_of(NT), kWarps * 32, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool MX>
 cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
-  const long long rows = (long long)p.b.max_q * p.group;
-  if (rows <= 8) return launch_rows<D, MX, 1>(p, st);
-  if (rows <= 16) return launch_rows<D, MX, 2>(p, st);
-  return launch_rows<D, MX, 4>(p, st);
+  const int nt = row_tiles(p);
+  return nt == 1 ? launch_rows<D, MX, 1>(p, st) : nt == 2 ? launch_rows<D, MX, 2>(p, st) : launch_rows<D, MX, 4>(p, st);
 }
 
 }  // namespace
@@ -464,7 +570,11 @@ namespace {
 bool use_tiles(const AttnParams &p) { return (long long)p.b.max_q * p.group > 32; }
 }  // namespace
 
-size_t attention_workspace(const AttnParams &p, int d) { return use_tiles(p) ? attention_tiles_workspace(p, d) : 16; }
+size_t attention_workspace(const AttnParams &p, int d) {
+  if (use_tiles(p)) return attention_tiles_workspace(p, d);
+  const int nt = row_tiles(p);
+  return kAttnCounterBytes + (size_t)blocks_of(nt) * 2 * 8 * nt * (d + 2) * sizeof(float);
+}
 
 cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t st) {
   if (use_tiles(p)) return launch_attention_tiles(p, d, fmt, st);

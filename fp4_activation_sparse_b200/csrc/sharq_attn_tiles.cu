@@ -207,15 +207,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// row / group for row < 2^32 / group (launch_attention's callers keep to that)
-__device__ __forceinline__ int over_group(const AttnParams &p, int row) { return (int)__umulhi((uint32_t)row, p.group_inv); }
-__device__ __forceinline__ int token_of(const AttnParams &p, int row) { return p.group == 1 ? row : over_group(p, row); }
+__device__ __forceinline__ int token_in(const AttnParams &p, int row) { return token_of(p.group, p.group_inv, row); }
 
 // ---------------------------------------------------------------- what a block works on
-// An item is 256 query rows of one key head of one sequence; an entry is an item of every head
-// (they cost the same). Steps of all items in a row, entry by entry, are cut into equal shares.
+// Items are 256 query rows of one key head of one sequence.
 // An item costs its key steps and kItemCost more (queries in, output out, the pipeline's start:
-// measured at about two steps); a share's place inside the first kItemCost units is its first step.
+// measured at about two steps).
 constexpr int kItemCost = 2;
 struct Range {
   int q0, rows, kv_len, first_pos, row0;
@@ -226,7 +223,7 @@ struct Range {
 struct Work {
   Range r;  // lo, hi, begin, end limited to the segment
   int seq, kh;
-  int parts, part, owner;  // segments of the item, this one's place, the block of the first
+  ItemParts parts;
 };
 
 __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt) {
@@ -244,8 +241,8 @@ __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt
     int k_lo = 0, k_hi = reach;
     const int last = min(w.rows, (t + 1) * kRows) - 1;
     if (p.causal) {
-      k_hi = min(k_hi, w.first_pos + token_of(p, w.row0 + max(last, 0)) + 1);
-      if (p.window > 0) k_lo = max(0, w.first_pos + token_of(p, w.row0 + t * kRows) - p.window + 1);
+      k_hi = min(k_hi, w.first_pos + token_in(p, w.row0 + max(last, 0)) + 1);
+      if (p.window > 0) k_lo = max(0, w.first_pos + token_in(p, w.row0 + t * kRows) - p.window + 1);
     }
     w.lo[t] = k_lo / kKeys;
     w.hi[t] = last >= t * kRows ? (max(k_hi, 0) + kKeys - 1) / kKeys : 0;
@@ -253,91 +250,6 @@ __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt
   }
   if (w.end == 0) w.begin = 0;
   return w;
-}
-
-// Where a block's share begins and ends, in steps and as an entry with its first step.
-struct Share {
-  long long total, blocks;  // steps of the launch, blocks that have a share
-  long long cut[2];         // begin and end of the share
-  long long first;          // first step of the entry that the share begins in
-  int entry, snap;
-};
-
-// A cut is moved to the item's edge where it would leave a piece of `snap` steps or fewer
-// (so that a cut inside an item always stands behind its first kItemCost units).
-__device__ __forceinline__ long long raw_cut(const Share &s, long long block) {
-  return block >= s.blocks ? s.total : block * s.total / s.blocks;
-}
-__device__ __forceinline__ long long snapped(long long x, long long p0, long long p1, int snap) {
-  return x - p0 <= kItemCost + snap ? p0 : p1 - x <= snap ? p1 : x;
-}
-
-// All threads: the entries' costs are summed in chunks of the block size, then the entries that
-// hold the share's two ends are found (from registers where one chunk holds every entry).
-__device__ __forceinline__ void find_share(const AttnParams &p, int row_tiles, Share *sh, long long *warp_sums) {
-  const long long entries = (long long)p.b.n_seq * row_tiles;
-  const int heads = p.c.kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long total = 0, before = 0, cost = 0, e = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long base = 0;
-    for (long long e0 = 0; e0 < entries; e0 += kThreads) {
-      if (pass == 0 || entries > kThreads) {
-        e = e0 + threadIdx.x;
-        cost = e < entries ? (long long)item_range(p, (int)(e / row_tiles), (int)(e % row_tiles)).cost() * heads : 0;
-        long long inc = cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-          if (lane >= o) inc += up;
-        }
-        __syncthreads();  // the sums of the chunk before have been read
-        if (lane == 31) warp_sums[warp] = inc;
-        __syncthreads();
-        before = base + inc - cost;
-        for (int x = 0; x < kThreads / 32; ++x) {
-          const long long v = warp_sums[x];
-          if (x < warp) before += v;
-          base += v;
-        }
-      }
-      if (pass == 1 && cost > 0) {
-        const int item = (int)(cost / heads);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const long long x = raw_cut(*sh, (long long)blockIdx.x + i);
-          if (x < before || x >= before + cost) continue;
-          const long long p0 = before + (x - before) / item * item;
-          const long long at = snapped(x, p0, p0 + item, sh->snap);
-          sh->cut[i] = at;
-          if (i == 0) sh->entry = (int)e, sh->first = before;
-        }
-      }
-    }
-    if (pass == 0) {
-      total = base;
-      if (threadIdx.x == 0) {
-        sh->total = total;
-        sh->blocks = min((long long)gridDim.x, max(1ll, total / (kItemCost + 2)));  // at least two steps each
-        sh->snap = (int)min(2ll, total / sh->blocks / 4);
-        sh->cut[0] = sh->cut[1] = total;  // ends that no entry holds
-        sh->entry = 0, sh->first = 0;
-      }
-      __syncthreads();
-    }
-  }
-  __syncthreads();
-}
-
-// The part of the item [p0, p1) that begins at `from`: how many parts it has, which one this is and
-// the block that holds the first.
-__device__ __forceinline__ void item_parts(const Share &s, long long p0, long long p1, long long from, Work &w) {
-  // cuts strictly inside: block numbers c with p0 + kItemCost + snap < raw_cut(c) < p1 - snap
-  const long long lo = ((p0 + kItemCost + s.snap + 1) * s.blocks + s.total - 1) / s.total;
-  long long hi = ((p1 - s.snap) * s.blocks + s.total - 1) / s.total - 1;
-  hi = min(hi, s.blocks - 1);
-  w.parts = hi >= lo ? (int)(hi - lo + 2) : 1;
-  w.owner = (int)lo - 1;
-  w.part = from == p0 ? 0 : (int)(blockIdx.x - lo + 1);
 }
 
 // ---------------------------------------------------------------- codes to float16 tiles
@@ -478,7 +390,7 @@ __device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles,
   x.kh = (int)((at - first) / cost);
   const long long p0 = first + (long long)x.kh * cost, p1 = p0 + cost;
   const long long to = min(sh.cut[1], p1);
-  item_parts(sh, p0, p1, at, x);
+  x.parts = item_parts<kItemCost>(sh, p0, p1, at);
   if (x.r.begin < x.r.end) {
     const int from = at == p0 ? x.r.begin : x.r.begin + (int)(at - p0) - kItemCost;
     const int until = x.r.begin + (int)(to - p0) - kItemCost;
@@ -503,7 +415,7 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w,
 #pragma unroll
   for (int x = 0; x < N; ++x) {
     const int r = t * kRows + row_base + x * RW + sub, row = w.r.row0 + r;
-    const int at = token_of(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
+    const int at = token_in(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
     v[x][0] = v[x][1] = make_uint4(0, 0, 0, 0);
     if (r < w.r.rows && token >= 0 && token < p.b.tokens) {
       const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)token * p.q_stride + head * D) + chunk;
@@ -576,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  find_share(p, row_tiles, &share, warp_sums);
+  find_share<kThreads, kItemCost>((long long)p.b.n_seq * row_tiles, p.c.kv_heads, kItemCost + 2, &share, warp_sums,
+                                  [&](long long e) { return item_range(p, (int)(e / row_tiles), (int)(e % row_tiles)).cost(); });
   if (share.cut[0] >= share.cut[1]) return;
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem_u32(&tmem_slot)), "r"(kTmemCols));
@@ -607,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       const int lo = t ? w.r.lo[1] : w.r.lo[0], hi = t ? w.r.hi[1] : w.r.hi[0];
       const int step0 = steps - w.r.begin;
       steps += w.r.end - w.r.begin;
-      const int kv_len = w.r.kv_len, pos = w.r.first_pos + token_of(p, w.r.row0 + t * kRows + r);
+      const int kv_len = w.r.kv_len, pos = w.r.first_pos + token_in(p, w.r.row0 + t * kRows + r);
       const int see_hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
       const int see_lo = p.causal && p.window > 0 ? pos - p.window : -1;
       const int last = max(min(w.r.rows, (t + 1) * kRows) - 1, 0);
-      const int tile_lo = w.r.first_pos + token_of(p, w.r.row0 + t * kRows), tile_hi = w.r.first_pos + token_of(p, w.r.row0 + last);
+      const int tile_lo = w.r.first_pos + token_in(p, w.r.row0 + t * kRows), tile_hi = w.r.first_pos + token_in(p, w.r.row0 + last);
       const float c = row_coef[t * kRows + r];  // of this warp's making; unused without steps
       float m = -INFINITY, l = 0.f;  // m: reference of the exponentials, in units of log2
       bool ok = true;
@@ -713,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       }
       const int row = w.r.row0 + t * kRows + r;  // row of the sequence's key head
       const bool live = t * kRows + r < w.r.rows;
-      const int at = token_of(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
+      const int at = token_in(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
       const bool real = live && token >= 0 && token < p.b.tokens;
       const float v_scale = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + w.kh);
       uint16_t *dst = p.y + ((size_t)token * p.q_heads + head) * D;
@@ -735,9 +648,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       const int tiles = p.b.max_q * p.group > kRows ? 2 : 1;
       float *const parts = reinterpret_cast<float *>(p.workspace + kAttnCounterBytes);
       auto part_at = [&](int j) {
-        return parts + (((size_t)(w.owner + j) * 2 + (j == 0 ? 1 : 0)) * tiles + t) * kRows * (D + 2) + r;
+        return parts + (((size_t)(w.parts.owner + j) * 2 + (j == 0 ? 1 : 0)) * tiles + t) * kRows * (D + 2) + r;
       };
-      float *mine = part_at(w.part);
+      float *mine = part_at(w.parts.index);
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t ov[32];
@@ -749,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
           for (int j = 0; j < 32; ++j) ov[j] = 0u;
         }
         const float *o = reinterpret_cast<const float *>(ov);
-        if (w.parts == 1) put(x, o, inv);
+        if (w.parts.count == 1) put(x, o, inv);
         else if (live) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) __stcg(mine + (32 * x + j) * kRows, o[j]);
@@ -759,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         tc_fence_before();
         mbar_arrive_warp(bar(bars.o_empty[t]));
       }
-      if (w.parts == 1) {
+      if (w.parts.count == 1) {
         put_lse(m, l);
         continue;
       }
@@ -767,9 +680,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       __threadfence();
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
       if (r == 0) {
-        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + 2 * w.owner + t;
+        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + 2 * w.parts.owner + t;
         const uint32_t before = atomicAdd(counter, 1u);
-        last_part[t] = before + 1 == (uint32_t)w.parts;
+        last_part[t] = before + 1 == (uint32_t)w.parts.count;
         if (last_part[t]) *counter = 0;  // ready for the next call
       }
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
@@ -777,9 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       __threadfence();
       if (!live) continue;
       float mm = -INFINITY, ll = 0.f;
-      for (int j = 0; j < w.parts; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
+      for (int j = 0; j < w.parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
       const float ref = mm == -INFINITY ? 0.f : mm;
-      for (int j = 0; j < w.parts; ++j)
+      for (int j = 0; j < w.parts.count; ++j)
         ll += __ldcg(part_at(j) + (D + 1) * kRows) * kv_ex2(__ldcg(part_at(j) + D * kRows) - ref);
       const float inv_all = ll == 0.f ? 0.f : v_scale / ll;
 #pragma unroll 1
@@ -787,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         float o[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = 0.f;
-        for (int j = 0; j < w.parts; ++j) {
+        for (int j = 0; j < w.parts.count; ++j) {
           const float *src = part_at(j);
           const float f = kv_ex2(__ldcg(src + D * kRows) - ref);
 #pragma unroll

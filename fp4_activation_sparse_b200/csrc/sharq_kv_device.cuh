@@ -37,4 +37,94 @@ __device__ __forceinline__ uint32_t kv_scales2(uint32_t two) {
   return d;
 }
 
+// row / group for row < 2^32 / group (the entry point keeps to that)
+__device__ __forceinline__ int token_of(int group, uint32_t group_inv, int row) {
+  return group == 1 ? row : (int)__umulhi((uint32_t)row, group_inv);
+}
+
+// ---------------------------------------------------------------- equal shares of a launch's work
+// An item is a block of query rows of one key head; an entry is the items of every head of the same
+// rows, which cost the same: their key steps, and ITEM more for what every item costs. The costs
+// of all items in a row, entry by entry, are cut into equal shares, one per block. A cut is moved to
+// the item's edge where it would leave a piece of `snap` steps or fewer, so that a cut inside an
+// item always stands behind its first ITEM units.
+struct Share {
+  long long total, blocks;  // cost of the launch, blocks that have a share
+  long long cut[2];         // begin and end of the share
+  long long first;          // where the entry that the share begins in begins
+  int entry, snap;
+};
+// An item's parts: how many, which one a block has, and the block of the first.
+struct ItemParts {
+  int count, index, owner;
+};
+
+__device__ __forceinline__ long long raw_cut(const Share &s, long long block) {
+  return block >= s.blocks ? s.total : block * s.total / s.blocks;
+}
+
+// All threads: the entries' costs are summed in chunks of the block size, then the entries that
+// hold the share's two ends are found (from registers where one chunk holds every entry).
+template <int THREADS, int ITEM, class Cost>
+__device__ __forceinline__ void find_share(long long entries, int heads, int least, Share *sh, long long *warp_sums,
+                                           Cost entry_cost) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long total = 0, before = 0, cost = 0, e = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+    for (long long e0 = 0; e0 < entries; e0 += THREADS) {
+      if (pass == 0 || entries > THREADS) {
+        e = e0 + threadIdx.x;
+        cost = e < entries ? (long long)entry_cost(e) * heads : 0;
+        long long inc = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+          if (lane >= o) inc += up;
+        }
+        __syncthreads();  // the sums of the chunk before have been read
+        if (lane == 31) warp_sums[warp] = inc;
+        __syncthreads();
+        before = base + inc - cost;
+        for (int x = 0; x < THREADS / 32; ++x) {
+          const long long v = warp_sums[x];
+          if (x < warp) before += v;
+          base += v;
+        }
+      }
+      if (pass == 1 && cost > 0) {
+        const int item = (int)(cost / heads);
+        for (int i = 0; i < 2; ++i) {
+          const long long x = raw_cut(*sh, (long long)blockIdx.x + i);
+          if (x < before || x >= before + cost) continue;
+          const long long p0 = before + (x - before) / item * item;
+          sh->cut[i] = x - p0 <= ITEM + sh->snap ? p0 : p0 + item - x <= sh->snap ? p0 + item : x;
+          if (i == 0) sh->entry = (int)e, sh->first = before;
+        }
+      }
+    }
+    if (pass == 0) {
+      total = base;
+      if (threadIdx.x == 0) {
+        sh->total = total;
+        sh->blocks = min((long long)gridDim.x, max(1ll, total / least));
+        sh->snap = (int)min(2ll, total / sh->blocks / 4);
+        sh->cut[0] = sh->cut[1] = total;  // ends that no entry holds
+        sh->entry = 0, sh->first = 0;
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+}
+
+// The parts of the item [p0, p1), of which this block has the one that begins at `from`. The cuts
+// inside it are those with p0 + ITEM + snap < raw_cut(block) < p1 - snap.
+template <int ITEM>
+__device__ __forceinline__ ItemParts item_parts(const Share &s, long long p0, long long p1, long long from) {
+  const long long lo = ((p0 + ITEM + s.snap + 1) * s.blocks + s.total - 1) / s.total;
+  const long long hi = min(((p1 - s.snap) * s.blocks + s.total - 1) / s.total - 1, s.blocks - 1);
+  return ItemParts{hi >= lo ? (int)(hi - lo + 2) : 1, from == p0 ? 0 : (int)(blockIdx.x - lo + 1), (int)lo - 1};
+}
+
 }  // namespace sharq
