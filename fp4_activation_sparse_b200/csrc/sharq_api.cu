@@ -679,10 +679,11 @@ int sharq_device_status(void *stream) {
   uint32_t prep_st = 0;
   cudaError_t e = sharq::read_and_clear_device_status(&st, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = sharq::read_and_clear_prep_status(&prep_st);
-  uint32_t attn_st = 0;
+  uint32_t attn_st = 0, rows_st = 0;
   if (e == cudaSuccess) e = sharq::read_and_clear_attn_status(&attn_st);
+  if (e == cudaSuccess) e = sharq::read_and_clear_attn_rows_status(&rows_st);
   if (e != cudaSuccess) return cuda_fail(e, "sharq_device_status");
-  st |= (int)(prep_st << 1) | (int)(attn_st << 2);
+  st |= (int)(prep_st << 1) | (int)(attn_st << 2) | (int)(rows_st << 3);
   if (st) return fail(SHARQ_ERR_TIMEOUT, "a bounded device wait gave up (code 0x%x)", st);
   g_err[0] = 0;
   return SHARQ_OK;

@@ -21,6 +21,9 @@
 #include "sharq_kv_device.cuh"
 
 namespace sharq {
+
+__device__ uint32_t g_attn_rows_status = 0;  // bit 0: a bounded wait gave up
+
 namespace {
 
 constexpr int kWarps = 8;
@@ -28,13 +31,23 @@ constexpr int kTile = 32;   // keys per step of a warp: two groups of the cache
 constexpr int kStagesA = 3;  // tiles in flight per warp
 constexpr int kItemCost = 8;  // what an item costs besides its tiles (queries, joining eight warps), in tiles
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// The warp waits for a stage's copies. After `limit_ns` the status word is set; the wait then goes
+// on, bounded again, so that no copy is in flight when the block ends.
+__device__ __forceinline__ void wait_copies(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !kv_mbar_try(bar, parity); ++i) {
+    if (i & 31u) continue;
+    const uint64_t t = kv_globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit_ns) atomicOr(&g_attn_rows_status, 1u);
+    if (t - t0 > limit_ns + kKvDrainLimitNs) break;
+  }
+  __syncwarp();
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -85,7 +98,7 @@ struct RowsKernel {
   static constexpr int KS = D / 16;  // matrix steps over D, and 16-row tiles of O^T
   static constexpr int kStageBytes = 2 * G.bytes;
   static constexpr int kRing = kWarps * kStagesA * kStageBytes;
-  static constexpr int kMerge = (kWarps / 2) * R * D * 4;
+  static constexpr int kMerge = kWarps * R * D * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
 };
 
@@ -117,426 +130,394 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
   using C = RowsKernel<D, MX, NT>;
   constexpr KvLayout G = C::G;
   constexpr int KS = C::KS;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sh_m[kWarps][C::R], sh_l[kWarps][C::R];
+  __shared__ uint64_t bars[kWarps][kStagesA];
+  __shared__ uint32_t last_part;
   __shared__ Share share;
   __shared__ long long warp_sums[kWarps];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (lane == 0) {
+    for (int i = 0; i < kStagesA; ++i) kv_mbar_init(kv_smem_u32(&bars[warp][i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   find_share<kWarps * 32, kItemCost>(p.b.n_seq, p.c.kv_heads, kWarps, &share, warp_sums,
                                      [&](long long e) { return rows_range(p, (int)e).cost(); });
+  const uint32_t ring = kv_smem_u32(smem) + warp * kStagesA * C::kStageBytes, bar0 = kv_smem_u32(&bars[warp][0]);
+  int load_stage = 0, use_stage = 0;  // the ring runs on from segment to segment
+  uint32_t use_parity = 0;
   int seq = share.entry;
   long long first = share.first;
   for (long long at = share.cut[0]; at < share.cut[1];) {
-  RowsRange w;
-  int cost;
-  for (;; ++seq) {  // sequences without new tokens have no items
-    w = rows_range(p, seq);
-    cost = w.cost();
-    if (at < first + (long long)cost * p.c.kv_heads) break;
-    first += (long long)cost * p.c.kv_heads;
-  }
-  const int kh = (int)((at - first) / cost);
-  const long long p0 = first + (long long)kh * cost, p1 = p0 + cost, to = min(share.cut[1], p1);
-  const ItemParts parts = item_parts<kItemCost>(share, p0, p1, at);
-  int t_lo = w.lo, t_hi = w.hi;
-  if (t_lo < t_hi) {
-    t_hi = w.lo + (int)(to - p0) - kItemCost;
-    if (at != p0) t_lo = w.lo + (int)(at - p0) - kItemCost;
-  }
-  at = to;
-  const int q0 = w.q0, rows = w.rows, kv_len = w.kv_len, first_pos = w.first_pos;
-  const int pos_lo = first_pos, pos_hi = first_pos + token_of(p.group, p.group_inv, rows - 1);
+    // ---- the next segment of the share
+    RowsRange w;
+    int cost;
+    for (;; ++seq) {  // sequences without new tokens have no items
+      w = rows_range(p, seq);
+      cost = w.cost();
+      if (at < first + (long long)cost * p.c.kv_heads) break;
+      first += (long long)cost * p.c.kv_heads;
+    }
+    const int kh = (int)((at - first) / cost);
+    const long long p0 = first + (long long)kh * cost, p1 = p0 + cost, to = min(share.cut[1], p1);
+    const ItemParts parts = item_parts<kItemCost>(share, p0, p1, at);
+    int t_lo = w.lo, t_hi = w.hi;
+    if (t_lo < t_hi) {
+      t_hi = w.lo + (int)(to - p0) - kItemCost;
+      if (at != p0) t_lo = w.lo + (int)(at - p0) - kItemCost;
+    }
+    at = to;
+    const int q0 = w.q0, rows = w.rows, kv_len = w.kv_len, first_pos = w.first_pos;
+    const int pos_lo = first_pos, pos_hi = first_pos + token_of(p.group, p.group_inv, rows - 1);
 
-  // ---- query fragments: lane (g, t) holds elements [D/4 * t, D/4 * (t + 1)) of row g of each n tile
-  uint32_t qf[NT][KS][2];
-  float coef[NT][2];  // score factor of columns 2t, 2t+1: softmax scale, key scale, the row's power of two
-  const float ks = MX || !p.c.k_scale ? 1.f : __ldg(p.c.k_scale + kh);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = n * 8 + g, tok = token_of(p.group, p.group_inv, r);
-    const int token = q0 + tok, head = kh * p.group + r - tok * p.group;
-    uint32_t raw[KS * 2];
-    if (r < rows && token >= 0 && token < p.b.tokens) {
-      const uint16_t *src = p.q + (size_t)token * p.q_stride + head * D + t * (D / 4);
-#pragma unroll
-      for (int i = 0; i < KS / 2; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-        raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+    // ---- copies: 32 keys a stage, one bulk copy per group of 16
+    const int page_groups = 1 << (p.c.page_shift - 4);
+    const int *table = p.b.page_table + (size_t)seq * p.b.max_pages;
+    // page id of the group `gi` of the sequence, -1 where it holds no keys
+    auto page_of = [&](int gi) -> int {
+      const int col = gi >> (p.c.page_shift - 4);
+      if (16 * gi >= kv_len || col >= p.b.max_pages) return -1;
+      const int page = __ldg(table + col);
+      return page < p.c.num_pages ? page : -1;
+    };
+    // 16 tiles' page ids in the lanes, lane 2i + h group h of the warp's tile base + i, and the next 16
+    auto page_ahead = [&](int i) { return page_of(2 * (t_lo + warp + kWarps * (i + (lane >> 1))) + (lane & 1)); };
+    int base = 0, ids = page_ahead(0), ids_next = page_ahead(16);
+    const int my_tiles = t_hi - t_lo > warp ? (t_hi - t_lo - warp + kWarps - 1) / kWarps : 0;
+    uint32_t valid_bits = 0;  // bits 2s, 2s+1: the groups of ring stage s hold keys
+    auto load = [&](int i) {
+      if (i >= my_tiles) return;
+      if (i - base >= 16) {
+        base += 16;
+        ids = ids_next;
+        ids_next = page_ahead(base + 16);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < KS * 2; ++i) raw[i] = 0u;
-    }
-    float am = 0.f;
-#pragma unroll
-    for (int i = 0; i < KS * 2; ++i) am = max3abs(am, bf16lo(raw[i]), bf16hi(raw[i]));
-    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    // the row's largest value moves to [2^12, 2^13): exact in float16 down to 2^-36 of it
-    const int e = max((int)(__float_as_uint(am) >> 23) - 127, -100);
-    const float up = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
-#pragma unroll
-    for (int i = 0; i < KS * 2; ++i) qf[n][i >> 1][i & 1] = kv_pack_half2(bf16lo(raw[i]) * up, bf16hi(raw[i]) * up);
-    const float down = __uint_as_float((uint32_t)(127 - 12 + e) << 23) * ks * p.scale_log2;
-    coef[n][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
-    coef[n][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
-  }
+      const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base) + 1);
+      const uint32_t there = (id0 >= 0 ? 1u : 0u) | (id1 >= 0 ? 2u : 0u);
+      valid_bits = (valid_bits & ~(3u << (2 * load_stage))) | (there << (2 * load_stage));
+      if (lane == 0) {
+        const uint32_t bar = bar0 + 8 * load_stage, dst = ring + load_stage * C::kStageBytes;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(__popc(there) * G.bytes) : "memory");
+        const int in_page = (2 * (t_lo + warp + kWarps * i)) & (page_groups - 1);
+        auto src = [&](int id, int gp) {
+          return p.c.pages + ((((size_t)id * p.c.kv_heads + kh) << (p.c.page_shift - 4)) + gp) * G.bytes;
+        };
+        if (id0 >= 0) bulk_load(dst, src(id0, in_page), G.bytes, bar);
+        if (id1 >= 0) bulk_load(dst + G.bytes, src(id1, (in_page + 1) & (page_groups - 1)), G.bytes, bar);
+      }
+      load_stage = load_stage == kStagesA - 1 ? 0 : load_stage + 1;
+    };
+    for (int i = 0; i < kStagesA - 1; ++i) load(i);
 
-  float o[KS][NT][4], m[NT][2], l[NT][2];
+    // ---- query fragments: lane (g, t) holds elements [D/4 * t, D/4 * (t + 1)) of row g of each n tile
+    uint32_t qf[NT][KS][2];
+    float coef[NT][2];  // score factor of columns 2t, 2t+1: softmax scale, key scale, the row's power of two
+    const float factor = (MX || !p.c.k_scale ? 1.f : __ldg(p.c.k_scale + kh)) * p.scale_log2;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    m[n][0] = m[n][1] = -INFINITY;
-    l[n][0] = l[n][1] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      const int r = n * 8 + g, tok = token_of(p.group, p.group_inv, r);
+      const int token = q0 + tok, head = kh * p.group + r - tok * p.group;
+      uint32_t raw[KS * 2];
+      if (r < rows && token >= 0 && token < p.b.tokens) {
+        const uint16_t *src = p.q + (size_t)token * p.q_stride + head * D + t * (D / 4);
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+          raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+        }
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[i][n][q] = 0.f;
-  }
-
-  const uint32_t ring = kv_smem_u32(smem) + warp * kStagesA * C::kStageBytes;
-  const int page_groups = 1 << (p.c.page_shift - 4);
-  const int *table = p.b.page_table + (size_t)seq * p.b.max_pages;
-  // page id of the group `gi` of the sequence, -1 where it holds no keys
-  auto page_of = [&](int gi) -> int {
-    const int col = gi >> (p.c.page_shift - 4);
-    if (16 * gi >= kv_len || col >= p.b.max_pages) return -1;
-    const int page = __ldg(table + col);
-    return page < p.c.num_pages ? page : -1;
-  };
-  // 16 tiles' page ids in the lanes: lane 2i + h has group h of the warp's tile base + i
-  auto page_ahead = [&](int i) { return page_of(2 * (t_lo + warp + kWarps * (i + (lane >> 1))) + (lane & 1)); };
-  int base = 0, ids = page_ahead(0), ids_next = page_ahead(16);
-  auto tile_ids = [&](int i, int &a, int &b) {  // i-th tile of this warp (in increasing order of calls)
-    if (i - base >= 16) {
-      base += 16;
-      ids = ids_next;
-      ids_next = page_ahead(base + 16);
+        for (int i = 0; i < KS * 2; ++i) raw[i] = 0u;
+      }
+      float am = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) am = max3abs(am, bf16lo(raw[i]), bf16hi(raw[i]));
+      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      // the row's largest value moves to [2^12, 2^13): exact in float16 down to 2^-36 of it; the sign of
+      // the score's factor goes into the query, so that maxima stay maxima
+      const int e = max((int)(__float_as_uint(am) >> 23) - 127, -100);
+      const float up = copysignf(__uint_as_float((uint32_t)(127 + 12 - e) << 23), factor);
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) qf[n][i >> 1][i & 1] = kv_pack_half2(bf16lo(raw[i]) * up, bf16hi(raw[i]) * up);
+      float down = __uint_as_float((uint32_t)(127 - 12 + e) << 23) * fabsf(factor);
+      if (down < 1e-37f) down = 1e-37f;  // 0 must not meet the masked -inf
+      coef[n][0] = __shfl_sync(0xFFFFFFFFu, down, 8 * t);
+      coef[n][1] = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4);
     }
-    a = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base));
-    b = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base) + 1);
-  };
-  const int my_tiles = t_hi - t_lo > warp ? (t_hi - t_lo - warp + kWarps - 1) / kWarps : 0;
-  uint32_t valid_bits = 0;  // bits 2s, 2s+1: the groups of ring stage s hold keys
-  auto load = [&](int i) {
-    if (i < my_tiles) {
-      int id[2];
-      tile_ids(i, id[0], id[1]);
-      const int s = i % kStagesA;
-      const int tile = t_lo + warp + kWarps * i;
-      valid_bits &= ~(3u << (2 * s));
+
+    float o[KS][NT][4], m[NT][2], l[NT][2];  // m: reference of the exponentials, in units of log2
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[i][n][q] = 0.f;
+    }
+
+    for (int it = 0; it < my_tiles; ++it) {
+      __syncwarp();  // every lane has left the stage that the next load overwrites
+      load(it + kStagesA - 1);
+      wait_copies(bar0 + 8 * use_stage, use_parity, p.limit_ns);
+      const uint32_t st = ring + use_stage * C::kStageBytes;
+      const int key0 = (t_lo + warp + kWarps * it) * kTile;
+      const uint32_t valid = (valid_bits >> (2 * use_stage)) & 3u;
+      use_stage = use_stage == kStagesA - 1 ? 0 : use_stage + 1;
+      if (use_stage == 0) use_parity ^= 1u;
+
+      // ---- S^T: two 16-key tiles
+      float sc[2][NT][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (id[h] < 0) continue;  // warp-uniform
-        valid_bits |= 1u << (2 * s + h);
-        const uint8_t *src = p.c.pages + ((((size_t)id[h] * p.c.kv_heads + kh) << (p.c.page_shift - 4)) +
-                                          ((2 * tile + h) & (page_groups - 1))) * G.bytes;
-        const uint32_t dst = ring + s * C::kStageBytes + h * G.bytes;
 #pragma unroll
-        for (int c = 0; c < (G.bytes / 16 + 31) / 32; ++c)
-          if (c * 32 + lane < G.bytes / 16) cp_async16(dst + (c * 32 + lane) * 16, src + (size_t)(c * 32 + lane) * 16);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sc[h][n][q] = 0.f;
+        uint32_t ca[KS / 2], cb[KS / 2];  // codes of rows g and g + 8: D/8 bytes from element D/4 * t
+        const uint32_t kc = st + h * G.bytes;
+        if (D == 128) {
+          lds128(kc + g * 64 + t * 16, ca);
+          lds128(kc + (g + 8) * 64 + t * 16, cb);
+        } else {
+          lds64(kc + g * 32 + t * 8, ca);
+          lds64(kc + (g + 8) * 32 + t * 8, cb);
+        }
+        // scales of the lane's elements: blocks of the first and second half of its matrix steps
+        uint32_t sa[2], sb[2];
+        const uint32_t kscale = kc + G.k_scales;
+        if (!MX && D == 128) {
+          const uint32_t a2 = kv_scales2<MX>(lds16(kscale + g * 8 + 2 * t)), b2 = kv_scales2<MX>(lds16(kscale + (g + 8) * 8 + 2 * t));
+          sa[0] = __byte_perm(a2, 0, 0x1010), sa[1] = __byte_perm(a2, 0, 0x3232);
+          sb[0] = __byte_perm(b2, 0, 0x1010), sb[1] = __byte_perm(b2, 0, 0x3232);
+        } else {
+          constexpr int NB = D / (MX ? 32 : 16);
+          const int blk = NB == 4 ? t : t >> 1;
+          const uint32_t two = kv_scales2<MX>(lds8(kscale + g * NB + blk) | (lds8(kscale + (g + 8) * NB + blk) << 8));
+          sa[0] = sa[1] = __byte_perm(two, 0, 0x1010);
+          sb[0] = sb[1] = __byte_perm(two, 0, 0x3232);
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t wa = ca[k >> 1], wb = cb[k >> 1];
+          const uint32_t fa = sa[2 * k / KS], fb = sb[2 * k / KS];
+          uint32_t a[4];
+          if (k & 1) a[0] = code_pair<2>(wa), a[1] = code_pair<2>(wb), a[2] = code_pair<3>(wa), a[3] = code_pair<3>(wb);
+          else a[0] = code_pair<0>(wa), a[1] = code_pair<0>(wb), a[2] = code_pair<1>(wa), a[3] = code_pair<1>(wb);
+          a[0] = mul2(a[0], fa), a[1] = mul2(a[1], fb), a[2] = mul2(a[2], fa), a[3] = mul2(a[3], fb);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(sc[h][n], a, qf[n][k][0], qf[n][k][1]);
+        }
       }
-    }
-    cp_commit();
-  };
-  for (int i = 0; i < kStagesA - 1; ++i) load(i);
-
-  for (int it = 0; it < my_tiles; ++it) {
-    __syncwarp();  // every lane has left the stage that the next load overwrites
-    load(it + kStagesA - 1);
-    cp_wait<kStagesA - 1>();
-    __syncwarp();
-    const int s = it % kStagesA;
-    const uint32_t st = ring + s * C::kStageBytes;
-    const int key0 = (t_lo + warp + kWarps * it) * kTile;
-    const uint32_t valid = (valid_bits >> (2 * s)) & 3u;
-
-    // ---- S^T: two 16-key tiles
-    float sc[2][NT][4];
+      // ---- masks
+      const bool whole = valid == 3u && key0 + kTile <= kv_len &&
+                         (!p.causal || (key0 + kTile - 1 <= pos_lo && (p.window <= 0 || key0 > pos_hi - p.window)));
+      if (!whole) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+          for (int c = 0; c < 2; ++c) {
+            const int pos = first_pos + token_of(p.group, p.group_inv, n * 8 + 2 * t + c);
+            const int hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
+            const int lo = p.causal && p.window > 0 ? pos - p.window : -1;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) sc[h][n][q] = 0.f;
-      uint32_t ca[KS / 2], cb[KS / 2];  // codes of rows g and g + 8: D/8 bytes from element D/4 * t
-      const uint32_t kc = st + h * G.bytes;
-      if (D == 128) {
-        lds128(kc + g * 64 + t * 16, ca);
-        lds128(kc + (g + 8) * 64 + t * 16, cb);
-      } else {
-        lds64(kc + g * 32 + t * 8, ca);
-        lds64(kc + (g + 8) * 32 + t * 8, cb);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int key = key0 + 16 * h + g + 8 * q;
+                if (!((valid >> h) & 1u) || key > hi || key <= lo) sc[h][n][2 * q + c] = -INFINITY;
+              }
+          }
       }
-      // scales of the lane's elements: blocks of the first and second half of its matrix steps
-      uint32_t sa[2], sb[2];
-      const uint32_t kscale = kc + G.k_scales;
-      if (!MX && D == 128) {
-        const uint32_t a2 = kv_scales2<MX>(lds16(kscale + g * 8 + 2 * t)), b2 = kv_scales2<MX>(lds16(kscale + (g + 8) * 8 + 2 * t));
-        sa[0] = __byte_perm(a2, 0, 0x1010), sa[1] = __byte_perm(a2, 0, 0x3232);
-        sb[0] = __byte_perm(b2, 0, 0x1010), sb[1] = __byte_perm(b2, 0, 0x3232);
-      } else {
-        constexpr int NB = D / (MX ? 32 : 16);
-        const int blk = NB == 4 ? t : t >> 1;
-        const uint32_t two = kv_scales2<MX>(lds8(kscale + g * NB + blk) | (lds8(kscale + (g + 8) * NB + blk) << 8));
-        sa[0] = sa[1] = __byte_perm(two, 0, 0x1010);
-        sb[0] = sb[1] = __byte_perm(two, 0, 0x3232);
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t wa = ca[k >> 1], wb = cb[k >> 1];
-        const uint32_t fa = sa[2 * k / KS], fb = sb[2 * k / KS];
-        uint32_t a[4];
-        if (k & 1) a[0] = code_pair<2>(wa), a[1] = code_pair<2>(wb), a[2] = code_pair<3>(wa), a[3] = code_pair<3>(wb);
-        else a[0] = code_pair<0>(wa), a[1] = code_pair<0>(wb), a[2] = code_pair<1>(wa), a[3] = code_pair<1>(wb);
-        a[0] = mul2(a[0], fa), a[1] = mul2(a[1], fb), a[2] = mul2(a[2], fa), a[3] = mul2(a[3], fb);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(sc[h][n], a, qf[n][k][0], qf[n][k][1]);
-      }
-    }
-    // ---- scores in units of log2, masked
-    const bool whole = valid == 3u && key0 + kTile <= kv_len &&
-                       (!p.causal || (key0 + kTile - 1 <= pos_lo && (p.window <= 0 || key0 > pos_hi - p.window)));
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sc[h][n][q] *= coef[n][q & 1];
-    if (!whole) {
+      // ---- exponentials against the reference at hand. It moves (and O and l are rescaled) only where
+      // a column's maximum is more than 2^8 above it: exponentials then stay far inside float16's range
+      float top[NT][2];
+      bool grew = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int pos = first_pos + token_of(p.group, p.group_inv, n * 8 + 2 * t + c);
-          const int hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
-          const int lo = p.causal && p.window > 0 ? pos - p.window : -1;
+          top[n][c] = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c])) * coef[n][c];
+          grew = grew || top[n][c] > m[n][c] + 8.f;
+        }
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = top[n][c];
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+            const float next = fmaxf(m[n][c], mx), f = next == -INFINITY ? 1.f : kv_ex2(m[n][c] - next);
+            m[n][c] = next;
+            l[n][c] *= f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) o[i][n][c] *= f, o[i][n][2 + c] *= f;
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float shift = m[n][c] == -INFINITY ? 0.f : -m[n][c];
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const int key = key0 + 16 * h + g + 8 * q;
-              if (!((valid >> h) & 1u) || key > hi || key <= lo) sc[h][n][2 * q + c] = -INFINITY;
+              const float e = kv_ex2(fmaf(sc[h][n][2 * q + c], coef[n][c], shift));
+              sc[h][n][2 * q + c] = e;
+              l[n][c] += e;
             }
         }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!((valid >> h) & 1u)) continue;  // warp-uniform; its probabilities are zero
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          pf[n][0] = trans8x8(kv_pack_half2(sc[h][n][0], sc[h][n][1]));
+          pf[n][1] = trans8x8(kv_pack_half2(sc[h][n][2], sc[h][n][3]));
+        }
+        const uint32_t vc = st + h * G.bytes + G.v_codes;
+        uint32_t v[2][4];  // [slot half][words]: D = 128: key 2t {lo, hi}, key 2t+1 {lo, hi}
+        lds128(vc + lane * 16, v[0]);
+        if (D == 128) lds128(vc + 512 + lane * 16, v[1]);
+        constexpr int per_run = (MX ? 32 : 16) / (D / 8);  // runs that share a block: 1, 2 or 4
+        uint32_t vs = lds32(st + h * G.bytes + G.v_scales + (g / per_run * 4 + t) * 4);
+        const int left = kv_len - (key0 + 16 * h);  // keys of the group that exist
+        if (left < 16) {  // scales of the others may be anything: zero keeps 0 * v from NaN
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (8 * (q >> 1) + 2 * t + (q & 1) >= left) vs &= ~(0xFFu << (8 * q));
+        }
+        const uint32_t s0 = kv_scales2<MX>(vs & 0xFFFFu), s1 = kv_scales2<MX>(vs >> 16);
+        uint32_t even[2][2], odd[2][2];  // [word][slot half]: nibbles of two keys of one element per byte
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t a = D == 128 ? v[hh][x] : v[0][2 * hh], b = D == 128 ? v[hh][2 + x] : v[0][2 * hh + 1];
+            even[x][hh] = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+            odd[x][hh] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+          }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          uint32_t a[4];
+          const uint32_t e0 = even[i >> 2][0], e1 = even[i >> 2][1], o0 = odd[i >> 2][0], o1 = odd[i >> 2][1];
+          switch (i & 3) {
+            case 0: a[0] = code_pair<0>(e0), a[1] = code_pair<0>(o0), a[2] = code_pair<0>(e1), a[3] = code_pair<0>(o1); break;
+            case 1: a[0] = code_pair<1>(e0), a[1] = code_pair<1>(o0), a[2] = code_pair<1>(e1), a[3] = code_pair<1>(o1); break;
+            case 2: a[0] = code_pair<2>(e0), a[1] = code_pair<2>(o0), a[2] = code_pair<2>(e1), a[3] = code_pair<2>(o1); break;
+            default: a[0] = code_pair<3>(e0), a[1] = code_pair<3>(o0), a[2] = code_pair<3>(e1), a[3] = code_pair<3>(o1);
+          }
+          a[0] = mul2(a[0], s0), a[1] = mul2(a[1], s0), a[2] = mul2(a[2], s1), a[3] = mul2(a[3], s1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(o[i][n], a, pf[n][0], pf[n][1]);
+        }
+      }
     }
-    // ---- running maximum and sum
+
+    // ---- join the warps: common maximum, every warp's O to shared memory, summed by all threads in
+    // the warps' order. Sixteen-byte units of a row are swapped by the row, so that a store's eight
+    // lanes (two runs of four rows) cover every bank.
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][2 + c]), fmaxf(sc[1][n][c], sc[1][n][2 + c]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-        const float top = fmaxf(m[n][c], mx);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float alpha = kv_ex2(m[n][c] - ref);
-        m[n][c] = top;
-        float sum = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float e = kv_ex2(sc[h][n][2 * q + c] - ref);
-            sc[h][n][2 * q + c] = e;
-            sum += e;
-          }
-        l[n][c] = l[n][c] * alpha + sum;
-        if (__any_sync(0xFFFFFFFFu, alpha != 1.f)) {
-#pragma unroll
-          for (int i = 0; i < KS; ++i) o[i][n][c] *= alpha, o[i][n][2 + c] *= alpha;
-        }
+        if (m[n][c] == INFINITY) l[n][c] = NAN;  // an infinite score has no softmax
+        l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 4);
+        l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 8);
+        l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 16);
+        if (g == 0) sh_m[warp][n * 8 + 2 * t + c] = m[n][c], sh_l[warp][n * 8 + 2 * t + c] = l[n][c];
       }
-    // ---- O^T += V^T P^T
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (!((valid >> h) & 1u)) continue;  // warp-uniform; its probabilities are zero
-      uint32_t pf[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        pf[n][0] = trans8x8(kv_pack_half2(sc[h][n][0], sc[h][n][1]));
-        pf[n][1] = trans8x8(kv_pack_half2(sc[h][n][2], sc[h][n][3]));
-      }
-      const uint32_t vc = st + h * G.bytes + G.v_codes;
-      uint32_t w[2][4];  // [slot half][words]: D = 128: key 2t {lo, hi}, key 2t+1 {lo, hi}
-      lds128(vc + lane * 16, w[0]);
-      if (D == 128) lds128(vc + 512 + lane * 16, w[1]);
-      constexpr int per_run = (MX ? 32 : 16) / (D / 8);  // runs that share a block: 1, 2 or 4
-      uint32_t vs = lds32(st + h * G.bytes + G.v_scales + (g / per_run * 4 + t) * 4);
-      const int left = kv_len - (key0 + 16 * h);  // keys of the group that exist
-      if (left < 16) {  // scales of the others may be anything: zero keeps 0 * v from NaN
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (8 * (q >> 1) + 2 * t + (q & 1) >= left) vs &= ~(0xFFu << (8 * q));
-      }
-      const uint32_t s0 = kv_scales2<MX>(vs & 0xFFFFu), s1 = kv_scales2<MX>(vs >> 16);
-      uint32_t even[2][2], odd[2][2];  // [word][slot half]: nibbles of two keys of one element per byte
-#pragma unroll
-      for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t a = D == 128 ? w[hh][x] : w[0][2 * hh], b = D == 128 ? w[hh][2 + x] : w[0][2 * hh + 1];
-          even[x][hh] = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
-          odd[x][hh] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
-        }
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        uint32_t a[4];
-        const uint32_t e0 = even[i >> 2][0], e1 = even[i >> 2][1], o0 = odd[i >> 2][0], o1 = odd[i >> 2][1];
-        switch (i & 3) {
-          case 0: a[0] = code_pair<0>(e0), a[1] = code_pair<0>(o0), a[2] = code_pair<0>(e1), a[3] = code_pair<0>(o1); break;
-          case 1: a[0] = code_pair<1>(e0), a[1] = code_pair<1>(o0), a[2] = code_pair<1>(e1), a[3] = code_pair<1>(o1); break;
-          case 2: a[0] = code_pair<2>(e0), a[1] = code_pair<2>(o0), a[2] = code_pair<2>(e1), a[3] = code_pair<2>(o1); break;
-          default: a[0] = code_pair<3>(e0), a[1] = code_pair<3>(o0), a[2] = code_pair<3>(e1), a[3] = code_pair<3>(o1);
-        }
-        a[0] = mul2(a[0], s0), a[1] = mul2(a[1], s0), a[2] = mul2(a[2], s1), a[3] = mul2(a[3], s1);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(o[i][n], a, pf[n][0], pf[n][1]);
-      }
-    }
-  }
-  cp_wait<0>();
-
-  // ---- merge the warps: common maximum, then a tree of sums in a fixed order
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 4);
-      l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 8);
-      l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], 16);
-      if (g == 0) sh_m[warp][n * 8 + 2 * t + c] = m[n][c], sh_l[warp][n * 8 + 2 * t + c] = l[n][c];
-    }
-  __syncthreads();
-  float top[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float mm = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sh_m[x][n * 8 + 2 * t + c]);
-      top[n][c] = mm;
-      const float ref = mm == -INFINITY ? 0.f : mm;
-      float sum = 0.f;
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) sum += sh_l[x][n * 8 + 2 * t + c] * kv_ex2(sh_m[x][n * 8 + 2 * t + c] - ref);
-      l[n][c] = sum;
-      const float f = kv_ex2(m[n][c] - ref);
-#pragma unroll
-      for (int i = 0; i < KS; ++i) o[i][n][c] *= f, o[i][n][2 + c] *= f;
-    }
-  float *slots = reinterpret_cast<float *>(smem);
-#pragma unroll
-  for (int half = kWarps / 2; half > 0; half >>= 1) {
-    if (warp >= half && warp < 2 * half) {
-      float *dst = slots + (size_t)(warp - half) * C::R * D + lane;
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) dst[((i * NT + n) * 4 + q) * 32] = o[i][n][q];
-    }
     __syncthreads();
-    if (warp < half) {
-      const float *src = slots + (size_t)warp * C::R * D + lane;
+    auto swap4 = [](int row) { return D == 128 ? (row >> 1) & 3 : ((row >> 1) & 1) | (((row >> 1) & 2) << 1); };
+    float4 *slots = reinterpret_cast<float4 *>(smem);
+    constexpr int F4 = D / 4;
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int c = 0; c < 2; ++c) {
+        const int row = n * 8 + 2 * t + c;
+        float mm = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) o[i][n][q] += src[((i * NT + n) * 4 + q) * 32];
-    }
+        for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sh_m[x][row]);
+        const float f = kv_ex2(m[n][c] - (mm == -INFINITY ? 0.f : mm));
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j)
+          slots[(warp * C::R + row) * F4 + ((g * (KS / 2) + j) ^ swap4(row))] =
+              make_float4(o[2 * j][n][c] * f, o[2 * j][n][2 + c] * f, o[2 * j + 1][n][c] * f, o[2 * j + 1][n][2 + c] * f);
+      }
     __syncthreads();
-  }
-  if (warp != 0) continue;  // the others begin the next segment
-  if (parts.count > 1) {
-    // parts: [block][first or not]: O in this lane order, then m and l by row
+    const float v_scale = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + kh);
+    // parts: [block][first or not]: O by row, then m and l
     float *const all = reinterpret_cast<float *>(p.workspace + kAttnCounterBytes);
     auto part_at = [&](int j) { return all + ((size_t)(parts.owner + j) * 2 + (j == 0 ? 1 : 0)) * C::R * (D + 2); };
-    float *mine = part_at(parts.index);
+    auto put = [&](int row, int i4, float4 v, float mm, float ll) {
+      const int tok = token_of(p.group, p.group_inv, row), token = q0 + tok, head = kh * p.group + row - tok * p.group;
+      if (token < 0 || token >= p.b.tokens) return;
+      const float inv = ll == 0.f ? 0.f : v_scale / ll;  // a NaN query stays NaN
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * inv, v.y * inv), b = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+      uint2 h;
+      h.x = *reinterpret_cast<const uint32_t *>(&a), h.y = *reinterpret_cast<const uint32_t *>(&b);
+      const size_t at_row = (size_t)token * p.q_heads + head;
+      *reinterpret_cast<uint2 *>(p.y + at_row * D + 4 * i4) = h;
+      if (i4 == 0 && p.lse) p.lse[at_row] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * 0.69314718055994531f;
+    };
+    for (int idx = threadIdx.x; idx < rows * F4; idx += kWarps * 32) {
+      const int row = idx / F4, i4 = idx % F4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+      for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sh_m[x][row]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) __stcg(mine + ((i * NT + n) * 4 + q) * 32 + lane, o[i][n][q]);
-    if (g == 0)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          __stcg(mine + C::R * D + 2 * (n * 8 + 2 * t + c), top[n][c]), __stcg(mine + C::R * D + 2 * (n * 8 + 2 * t + c) + 1, l[n][c]);
-    __threadfence();
-    __syncwarp();
-    uint32_t before = 0;
-    if (lane == 0) {
-      uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + parts.owner;
-      before = atomicAdd(counter, 1u);
-      if (before + 1 == (uint32_t)parts.count) *counter = 0;  // ready for the next call
-    }
-    if (__shfl_sync(0xFFFFFFFFu, before, 0) + 1 != (uint32_t)parts.count) continue;
-    __threadfence();
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float mm = -INFINITY;
-        for (int j = 0; j < parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + C::R * D + 2 * (n * 8 + 2 * t + c)));
-        top[n][c] = mm;
-        l[n][c] = 0.f;
+      for (int x = 0; x < kWarps; ++x) {
+        ll += sh_l[x][row] * kv_ex2(sh_m[x][row] - (mm == -INFINITY ? 0.f : mm));
+        const float4 u = slots[(x * C::R + row) * F4 + (i4 ^ swap4(row))];
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
       }
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[i][n][q] = 0.f;
-    for (int j = 0; j < parts.count; ++j) {
-      const float *src = part_at(j);
-      float f[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float *ml = src + C::R * D + 2 * (n * 8 + 2 * t + c);
-          f[n][c] = kv_ex2(__ldcg(ml) - (top[n][c] == -INFINITY ? 0.f : top[n][c]));
-          l[n][c] += f[n][c] * __ldcg(ml + 1);
+      if (parts.count == 1) {
+        put(row, i4, v, mm, ll);
+      } else {
+        float *mine = part_at(parts.index);
+        __stcg(reinterpret_cast<float4 *>(mine) + idx, v);
+        if (i4 == 0) __stcg(reinterpret_cast<float2 *>(mine + C::R * D) + row, make_float2(mm, ll));
+      }
+    }
+    if (parts.count > 1) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + parts.owner;
+        last_part = atomicAdd(counter, 1u) + 1 == (uint32_t)parts.count;
+        if (last_part) *counter = 0;  // ready for the next call
+      }
+      __syncthreads();
+      if (last_part) {
+        __threadfence();
+        for (int idx = threadIdx.x; idx < rows * F4; idx += kWarps * 32) {
+          const int row = idx / F4, i4 = idx % F4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          float mm = -INFINITY, ll = 0.f;
+          for (int j = 0; j < parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + C::R * D + 2 * row));
+          for (int j = 0; j < parts.count; ++j) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_at(j) + C::R * D) + row);
+            const float f = kv_ex2(ml.x - (mm == -INFINITY ? 0.f : mm));
+            const float4 u = __ldcg(reinterpret_cast<const float4 *>(part_at(j)) + idx);
+            ll += ml.y * f;
+            v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+          }
+          put(row, i4, v, mm, ll);
         }
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) o[i][n][q] = fmaf(f[n][q & 1], __ldcg(src + ((i * NT + n) * 4 + q) * 32 + lane), o[i][n][q]);
-    }
-  }
-  const float vs = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + kh);
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = n * 8 + 2 * t + c, tok = token_of(p.group, p.group_inv, r);
-      const int token = q0 + tok, head = kh * p.group + r - tok * p.group;
-      if (r >= rows || token < 0 || token >= p.b.tokens) continue;
-      const float inv = l[n][c] == 0.f ? 0.f : vs / l[n][c];  // a NaN query stays NaN
-      // the lane's run of D/8 elements: rows g (even elements) and g + 8 (odd) of each 16-row tile
-      uint32_t out[KS];
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(o[i][n][c] * inv, o[i][n][2 + c] * inv);
-        out[i] = *reinterpret_cast<const uint32_t *>(&h2);
       }
-      uint16_t *dst = p.y + ((size_t)token * p.q_heads + head) * D + g * (D / 8);
-#pragma unroll
-      for (int i = 0; i < KS / 4; ++i)
-        reinterpret_cast<uint4 *>(dst)[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
-      if (p.lse && g == 0)
-        p.lse[(size_t)token * p.q_heads + head] =
-            l[n][c] == 0.f ? -INFINITY : (top[n][c] + __log2f(l[n][c])) * 0.69314718055994531f;
     }
+    // the next segment's copies overwrite what was just read
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
   }
 }
 
@@ -580,6 +561,13 @@ cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t s
   if (use_tiles(p)) return launch_attention_tiles(p, d, fmt, st);
   if (d == 128) return fmt ? launch_d<128, true>(p, st) : launch_d<128, false>(p, st);
   return fmt ? launch_d<64, true>(p, st) : launch_d<64, false>(p, st);
+}
+
+cudaError_t read_and_clear_attn_rows_status(uint32_t *status) {
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_attn_rows_status, sizeof *status);
+  if (e != cudaSuccess || *status == 0) return e;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_attn_rows_status, &zero, sizeof zero);
 }
 
 }  // namespace sharq

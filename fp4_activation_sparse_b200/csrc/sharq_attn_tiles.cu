@@ -46,7 +46,6 @@ constexpr int kRows = 128;  // query rows of a tile
 constexpr int kKeys = 128;  // keys of a step
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;  // S of tile t, half h at 128 t + 64 h (P over its first 32); O at 256 + 128 t
-constexpr uint64_t kDrainLimitNs = 4000000000ull;
 constexpr int kValidRing = 4;
 
 template <int D>
@@ -64,9 +63,6 @@ struct Bars {
 };
 constexpr int kWorkReaders = 8 + 4 + 2;  // warps
 
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -75,26 +71,12 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ uint64_t globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
 // Gives up after `limit_ns`, or when another role of the block already did.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t *abort_flag) {
   uint64_t t0 = 0;
-  for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
+  for (uint32_t i = 1; !kv_mbar_try(bar, parity); ++i) {
     if (i & 31u) continue;
-    const uint64_t t = globaltimer();
+    const uint64_t t = kv_globaltimer();
     if (t0 == 0) t0 = t;
     if (t - t0 > limit_ns) {
       *abort_flag = 1u;
@@ -108,9 +90,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                                volatile uint32_t *abort_flag) {
   uint64_t t0 = 0;
-  for (uint32_t i = 1; !__all_sync(0xFFFFFFFFu, mbar_try(bar, parity)); ++i) {
+  for (uint32_t i = 1; !__all_sync(0xFFFFFFFFu, kv_mbar_try(bar, parity)); ++i) {
     if (i & 31u) continue;
-    const uint64_t t = globaltimer();
+    const uint64_t t = kv_globaltimer();
     if (t0 == 0) t0 = t;
     if (t - t0 > limit_ns) {
       *abort_flag = 1u;
@@ -471,20 +453,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bars.work_full[i]), 1);
-      mbar_init(bar(bars.work_empty[i]), kWorkReaders);
-      mbar_init(bar(bars.q_full[i]), 4);
-      mbar_init(bar(bars.k_full[i]), 4);
-      mbar_init(bar(bars.v_full[i]), 4);
-      mbar_init(bar(bars.k_empty[i]), 2);
-      mbar_init(bar(bars.v_empty[i]), 2);
+      kv_mbar_init(bar(bars.work_full[i]), 1);
+      kv_mbar_init(bar(bars.work_empty[i]), kWorkReaders);
+      kv_mbar_init(bar(bars.q_full[i]), 4);
+      kv_mbar_init(bar(bars.k_full[i]), 4);
+      kv_mbar_init(bar(bars.v_full[i]), 4);
+      kv_mbar_init(bar(bars.k_empty[i]), 2);
+      kv_mbar_init(bar(bars.v_empty[i]), 2);
       for (int h = 0; h < 2; ++h) {
-        mbar_init(bar(bars.s_full[i][h]), 1);
-        mbar_init(bar(bars.p_full[i][h]), 4);
-        mbar_init(bar(bars.pv_done[i][h]), 1);
+        kv_mbar_init(bar(bars.s_full[i][h]), 1);
+        kv_mbar_init(bar(bars.p_full[i][h]), 4);
+        kv_mbar_init(bar(bars.pv_done[i][h]), 1);
       }
-      mbar_init(bar(bars.o_empty[i]), 4);
-      mbar_init(bar(bars.drain[i]), 1);
+      kv_mbar_init(bar(bars.o_empty[i]), 4);
+      kv_mbar_init(bar(bars.drain[i]), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -837,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
     if (lead) {
       tc_commit(bar(bars.drain[t]));
       volatile uint32_t never = 0;
-      mbar_wait(bar(bars.drain[t]), 0, kDrainLimitNs, &never);
+      mbar_wait(bar(bars.drain[t]), 0, kKvDrainLimitNs, &never);
     }
     __syncwarp();
   } else {

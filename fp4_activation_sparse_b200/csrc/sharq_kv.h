@@ -99,6 +99,7 @@ constexpr int kAttnCounterBytes = 8192;
 size_t attention_tiles_workspace(const AttnParams &p, int d);
 cudaError_t launch_attention_tiles(const AttnParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t read_and_clear_attn_status(uint32_t *status);
+cudaError_t read_and_clear_attn_rows_status(uint32_t *status);
 size_t attention_workspace(const AttnParams &p, int d);
 cudaError_t launch_norm_residual(const NormResidualParams &p, cudaStream_t st);
 
