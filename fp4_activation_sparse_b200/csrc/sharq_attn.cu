@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0) {
-    for (int i = 0; i < kStagesA; ++i) kv_mbar_init(kv_smem_u32(&bars[warp][i]), 1);
+    for (int i = 0; i < kStagesA; ++i) kv_mbar_init(kv_smem_u32(&bars[warp][i]), 2);  // a lane per group
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   find_share<kWarps * 32, kItemCost>(p.b.n_seq, p.c.kv_heads, kWarps, &share, warp_sums,
@@ -181,30 +181,33 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       const int page = __ldg(table + col);
       return page < p.c.num_pages ? page : -1;
     };
-    // 16 tiles' page ids in the lanes, lane 2i + h group h of the warp's tile base + i, and the next 16
+    // Lane 2i + h has group h of the warp's tile base + i, its place in memory and the page id of the
+    // group 16 tiles on, and issues its copy itself.
     auto page_ahead = [&](int i) { return page_of(2 * (t_lo + warp + kWarps * (i + (lane >> 1))) + (lane & 1)); };
-    int base = 0, ids = page_ahead(0), ids_next = page_ahead(16);
+    auto place = [&](int i, int id) {
+      const int in_page = (2 * (t_lo + warp + kWarps * (i + (lane >> 1))) + (lane & 1)) & (page_groups - 1);
+      return p.c.pages + ((((size_t)max(id, 0) * p.c.kv_heads + kh) << (p.c.page_shift - 4)) + in_page) * G.bytes;
+    };
+    int base = 0, id = page_ahead(0), id_next = page_ahead(16);
+    const uint8_t *grp = place(0, id);
+    uint32_t there = __ballot_sync(0xFFFFFFFFu, id >= 0);
     const int my_tiles = t_hi - t_lo > warp ? (t_hi - t_lo - warp + kWarps - 1) / kWarps : 0;
     uint32_t valid_bits = 0;  // bits 2s, 2s+1: the groups of ring stage s hold keys
     auto load = [&](int i) {
       if (i >= my_tiles) return;
       if (i - base >= 16) {
         base += 16;
-        ids = ids_next;
-        ids_next = page_ahead(base + 16);
+        id = id_next;
+        id_next = page_ahead(base + 16);
+        grp = place(base, id);
+        there = __ballot_sync(0xFFFFFFFFu, id >= 0);
       }
-      const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (i - base) + 1);
-      const uint32_t there = (id0 >= 0 ? 1u : 0u) | (id1 >= 0 ? 2u : 0u);
-      valid_bits = (valid_bits & ~(3u << (2 * load_stage))) | (there << (2 * load_stage));
-      if (lane == 0) {
-        const uint32_t bar = bar0 + 8 * load_stage, dst = ring + load_stage * C::kStageBytes;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(__popc(there) * G.bytes) : "memory");
-        const int in_page = (2 * (t_lo + warp + kWarps * i)) & (page_groups - 1);
-        auto src = [&](int id, int gp) {
-          return p.c.pages + ((((size_t)id * p.c.kv_heads + kh) << (p.c.page_shift - 4)) + gp) * G.bytes;
-        };
-        if (id0 >= 0) bulk_load(dst, src(id0, in_page), G.bytes, bar);
-        if (id1 >= 0) bulk_load(dst + G.bytes, src(id1, (in_page + 1) & (page_groups - 1)), G.bytes, bar);
+      const int pair = i - base;
+      valid_bits = (valid_bits & ~(3u << (2 * load_stage))) | (((there >> (2 * pair)) & 3u) << (2 * load_stage));
+      if (lane >> 1 == pair) {
+        const uint32_t bar = bar0 + 8 * load_stage;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(id >= 0 ? G.bytes : 0) : "memory");
+        if (id >= 0) bulk_load(ring + load_stage * C::kStageBytes + (lane & 1) * G.bytes, grp, G.bytes, bar);
       }
       load_stage = load_stage == kStagesA - 1 ? 0 : load_stage + 1;
     };
