@@ -148,8 +148,8 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object (3 us)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -406,23 +406,27 @@ def _tensor(t, name: str, dtype, device, shape=None, contiguous: bool = True):
     """Checks one device tensor argument (`shape` entries of None are free)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _reject(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         _reject(f"{name} must be {dtype} (got {t.dtype})")
     if device is not None and t.device != device:
         _reject(f"{name} is on {t.device}, the call on {device}")
-    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        _reject(f"{name} must have shape {tuple('any' if n is None else n for n in shape)} (got {tuple(t.shape)})")
+    if shape is not None and t.shape != shape:
+        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+            _reject(f"{name} must have shape {tuple('any' if n is None else n for n in shape)} (got {tuple(t.shape)})")
     if contiguous and not t.is_contiguous():
         _reject(f"{name} must be contiguous")
 
 
 def _rows(t: torch.Tensor, name: str) -> int:
     """Distance in elements between the first-axis rows of `t`, which must itself be dense."""
-    n = 1
+    n = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
+    if t.is_contiguous():
+        return n
+    dense = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and stride != n:
+        if size > 1 and stride != dense:
             _reject(f"{name} may be strided along its first axis only")
-        n *= size
+        dense *= size
     return t.stride(0) if t.shape[0] > 1 else n
 
 
@@ -600,8 +604,8 @@ def sharq_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, causal: boo
     alloc_attention_workspace (allocated here if omitted)."""
     dev = _same_device(cache, batch)
     d = cache.head_dim
-    _tensor(q, "q", torch.bfloat16, dev, (batch.tokens, None, d), contiguous=False)
-    hq = q.shape[1]
+    hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
+    _tensor(q, "q", torch.bfloat16, dev, (batch.tokens, hq, d), contiguous=False)
     stride = _rows(q, "q")
     if y is None:
         y = torch.empty(batch.tokens, hq, d, dtype=torch.bfloat16, device=dev)

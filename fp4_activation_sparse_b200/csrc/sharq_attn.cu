@@ -535,8 +535,8 @@ template <int D, bool MX, int NT>
 cudaError_t launch_rows(const AttnParams &p, cudaStream_t st) {
   using C = RowsKernel<D, MX, NT>;
   auto kernel = attn_rows_kernel<D, MX, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
+  static SmemOnce once;
+  if (cudaError_t e = once.set(kernel, C::kSmem)) return e;
   kernel<<<blocks_of(NT), kWarps * 32, C::kSmem, st>>>(p);
   return cudaGetLastError();
 }

@@ -850,8 +850,8 @@ int row_tiles(const AttnParams &p) {
 template <int D, bool MX>
 cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
   auto kernel = attn_tiles_kernel<D, MX>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TileSmem<D>::kTotal);
-  if (e != cudaSuccess) return e;
+  static SmemOnce once;
+  if (cudaError_t e = once.set(kernel, TileSmem<D>::kTotal)) return e;
   kernel<<<sm_count(), kThreads, TileSmem<D>::kTotal, st>>>(p, row_tiles(p));
   return cudaGetLastError();
 }

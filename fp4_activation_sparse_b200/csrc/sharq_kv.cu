@@ -1,6 +1,7 @@
 // The paged FP4 key/value cache: appending a call's keys and values (with the per-head
 // normalization and the position rotation of q and k on the way) and reading rows back.
 #include "sharq_common.cuh"
+#include "sharq_internal.h"
 #include "sharq_kv.h"
 
 namespace sharq {
@@ -35,54 +36,70 @@ struct TokenPlace {
   long long page;     // -1: no place in the cache
 };
 
-// All threads of the block find the sequence of one token: the count of sequences that end at
-// or before it (one pass over cu_q, not a chain of dependent loads).
-__device__ __forceinline__ TokenPlace find_token(const KvBatchView &b, const KvCacheView &c, int token) {
+// The places of `n` consecutive tokens. The block counts the sequences that end at or before the
+// first (one pass over cu_q, not a chain of dependent loads); a thread per token searches on.
+constexpr int kMaxTokens = 8;
+__device__ __forceinline__ void find_tokens(const KvBatchView &b, const KvCacheView &c, int token0, int n, TokenPlace *out) {
   int seq = 0;
   for (int i0 = 0; i0 < b.n_seq; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
-    seq += __syncthreads_count(i < b.n_seq && __ldg(b.cu_q + i + 1) <= token);
+    seq += __syncthreads_count(i < b.n_seq && __ldg(b.cu_q + i + 1) <= token0);
   }
-  TokenPlace t{0, 0, -1};
-  if (seq >= b.n_seq || token < __ldg(b.cu_q)) return t;
-  t.in_use = 1;
-  t.pos = __ldg(b.kv_len + seq) - __ldg(b.cu_q + seq + 1) + token;
-  const int col = t.pos >> c.page_shift;
-  if (t.pos >= 0 && col < b.max_pages) {
-    const int page = __ldg(b.page_table + (size_t)seq * b.max_pages + col);
-    if (page >= 0 && page < c.num_pages) t.page = page;
+  if (threadIdx.x < n) {
+    const int token = token0 + threadIdx.x;
+    int hi = b.n_seq;  // the first sequence that ends behind the token is in [seq, hi]
+    while (seq < hi) {
+      const int mid = (seq + hi) >> 1;
+      if (__ldg(b.cu_q + mid + 1) <= token) seq = mid + 1;
+      else hi = mid;
+    }
+    TokenPlace t{0, 0, -1};
+    if (seq < b.n_seq && token >= __ldg(b.cu_q)) {
+      t.in_use = 1;
+      t.pos = __ldg(b.kv_len + seq) - __ldg(b.cu_q + seq + 1) + token;
+      const int col = t.pos >> c.page_shift;
+      if (t.pos >= 0 && col < b.max_pages) {
+        const int page = __ldg(b.page_table + (size_t)seq * b.max_pages + col);
+        if (page >= 0 && page < c.num_pages) t.page = page;
+      }
+    }
+    out[threadIdx.x] = t;
   }
-  return t;
+  __syncthreads();
 }
 
-// Append: one block per token, D/8 lanes per head, eight elements per lane; the lane of the
-// rotation's partner elements loads them itself (they are in L1), so no lane waits for another
+// Append: a block per one to eight tokens, D/8 lanes per head, eight elements per lane; the lane of
+// the rotation's partner elements loads them itself (they are in L1), so no lane waits for another
 // except for the block maxima. cos and sin are formed once per token from the 64-bit angle and
-// rounded once. Bound by the bytes of the row (read once, q written once); the 64-bit sine and
-// cosine of D/2 angles per token run beside the loads.
+// rounded once. Bound by the bytes of the row (read once, q written once); several tokens per block
+// share the latency of finding their places and of the sines.
 template <int D, bool MX>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p, int per_block) {
   constexpr int L = D / 8;  // lanes per head
   constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
   constexpr int NB = D / (MX ? 32 : 16);
-  __shared__ float2 turn[D / 2];
-  const int token = blockIdx.x;
-  const TokenPlace tp = find_token(p.b, p.c, token);
-  if (!tp.in_use) return;
-  for (int i = threadIdx.x; i < p.rot_half; i += blockDim.x) {
+  __shared__ float2 turns[kMaxTokens][D / 2];
+  __shared__ TokenPlace places[kMaxTokens];
+  const int token0 = blockIdx.x * per_block, n = min(per_block, p.b.tokens - token0);
+  find_tokens(p.b, p.c, token0, n, places);
+  for (int i = threadIdx.x; i < n * p.rot_half; i += blockDim.x) {
+    const int x = i / p.rot_half, j = i - x * p.rot_half;
     double s, c;
-    sincos((double)tp.pos * (double)__ldg(p.inv_freq + i), &s, &c);
-    turn[i] = make_float2(__double2float_rn(c), __double2float_rn(s));
+    sincos((double)places[x].pos * (double)__ldg(p.inv_freq + j), &s, &c);
+    turns[x][j] = make_float2(__double2float_rn(c), __double2float_rn(s));
   }
   __syncthreads();
   const int kvh = p.c.kv_heads, heads = p.q_heads + 2 * kvh;
   const int j = threadIdx.x % L, e0 = 8 * j;
-  const uint16_t *row = p.qkv + (size_t)token * p.row_stride;
   // whole warps stay in the loop: the shuffles below name every lane
-  for (int h0 = 0; h0 < heads; h0 += blockDim.x / L) {
-    const int head = h0 + threadIdx.x / L;
-    const bool live = head < heads;
-    const bool is_q = head < p.q_heads, is_k = !is_q && head < p.q_heads + kvh;
+#pragma unroll 2
+  for (int i0 = 0; i0 < n * heads; i0 += blockDim.x / L) {
+    const int i = i0 + threadIdx.x / L, x_tok = i / heads, head = i - x_tok * heads, token = token0 + x_tok;
+    const TokenPlace tp = places[min(x_tok, n - 1)];
+    const bool live = i < n * heads && tp.in_use;
+    const uint16_t *row = p.qkv + (size_t)token * p.row_stride;
+    const float2 *turn = turns[min(x_tok, n - 1)];
+    const bool is_q = live && head < p.q_heads, is_k = live && !is_q && head < p.q_heads + kvh;
     float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     uint4 w = make_uint4(0, 0, 0, 0);
     if (live) w = ld128(row + (size_t)head * D + e0);
@@ -175,67 +192,88 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   }
 }
 
-// Read: one block per token; a lane turns eight codes and their scale into values.
+// Read: a block per one to eight tokens; a lane turns eight codes and their scale into values, four
+// such units in flight at once.
 template <int D, bool MX>
-__global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams p) {
-  constexpr int L = D / 8;
+__global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams p, int per_block) {
+  constexpr int L = D / 8, U = 4;
   constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
   constexpr int NB = D / (MX ? 32 : 16);
-  const int token = blockIdx.x;
-  const TokenPlace tp = find_token(p.b, p.c, token);
-  if (!tp.in_use) return;
-  const int kvh = p.c.kv_heads;
-  const int in_page = tp.pos & ((1 << p.c.page_shift) - 1), r = in_page & 15;
-  for (int i = threadIdx.x; i < 2 * kvh * L; i += blockDim.x) {
-    const int j = i % L, head = (i / L) % kvh, is_v = i / (L * kvh), e0 = 8 * j;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (tp.page >= 0) {
+  __shared__ TokenPlace places[kMaxTokens];
+  const int token0 = blockIdx.x * per_block, n = min(per_block, p.b.tokens - token0);
+  find_tokens(p.b, p.c, token0, n, places);
+  const int kvh = p.c.kv_heads, units = 2 * kvh * L;
+  for (int i0 = threadIdx.x; i0 < n * units; i0 += U * blockDim.x) {
+    uint32_t codes[U], sb[U];
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      const int i = i0 + y * blockDim.x;
+      codes[y] = sb[y] = 0u;
+      if (i >= n * units) continue;
+      const int x = i / units, in = i - x * units, j = in % L, is_v = in >= kvh * L, head = in / L - is_v * kvh, e0 = 8 * j;
+      const TokenPlace tp = places[x];
+      if (tp.page < 0) continue;
+      const int in_page = tp.pos & ((1 << p.c.page_shift) - 1), r = in_page & 15, blk = e0 / (MX ? 32 : 16);
       const uint8_t *grp =
           p.c.pages + ((((size_t)tp.page * kvh + head) << (p.c.page_shift - 4)) + (in_page >> 4)) * G.bytes;
-      const int blk = e0 / (MX ? 32 : 16);
       const int at = is_v ? G.v_codes + kv_v_place(D, r, e0 / (D / 8)) + (D == 128 ? 4 * (j & 1) : 0) : r * (D / 2) + 4 * j;
-      const uint32_t codes = *reinterpret_cast<const uint32_t *>(grp + at);
-      const uint32_t sb = grp[is_v ? G.v_scales + kv_v_scale_place(r, blk) : G.k_scales + r * NB + blk];
+      codes[y] = *reinterpret_cast<const uint32_t *>(grp + at);
+      sb[y] = grp[is_v ? G.v_scales + kv_v_scale_place(r, blk) : G.k_scales + r * NB + blk];
+    }
+#pragma unroll
+    for (int y = 0; y < U; ++y) {
+      const int i = i0 + y * blockDim.x;
+      if (i >= n * units) continue;
+      const int x = i / units, in = i - x * units, j = in % L, is_v = in >= kvh * L, head = in / L - is_v * kvh, e0 = 8 * j;
+      if (!places[x].in_use) continue;
       const float *sp = is_v ? p.c.v_scale : p.c.k_scale;
-      const float s = MX ? 1.f : sp ? __ldg(sp + head) : 1.f;
-      const float b = MX ? e8m0_to_f32(sb) : e4m3_to_f32(sb);
+      const float s = MX ? 1.f : sp ? __ldg(sp + head) : 1.f, b = MX ? e8m0_to_f32(sb[y]) : e4m3_to_f32(sb[y]);
       uint32_t h[4];
-      cvt_e2m1x8_to_f16x2(codes, h);
+      cvt_e2m1x8_to_f16x2(codes[y], h);
+      float v[8];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float2 f = half2_bits_to_float2(h[q]);
-        x[2 * q] = __fmul_rn(__fmul_rn(f.x, b), s);
-        x[2 * q + 1] = __fmul_rn(__fmul_rn(f.y, b), s);
+        v[2 * q] = __fmul_rn(__fmul_rn(f.x, b), s);
+        v[2 * q + 1] = __fmul_rn(__fmul_rn(f.y, b), s);
+      }
+      const size_t o = ((size_t)(token0 + x) * kvh + head) * D + e0;
+      void *out = is_v ? p.v_out : p.k_out;
+      if (p.out_f32) {
+        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
+        f[0] = make_float4(v[0], v[1], v[2], v[3]);
+        f[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + o) = pack8_bf16(v);
       }
     }
-    const size_t o = ((size_t)token * kvh + head) * D + e0;
-    void *out = is_v ? p.v_out : p.k_out;
-    if (p.out_f32) {
-      float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
-      f[0] = make_float4(x[0], x[1], x[2], x[3]);
-      f[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + o) = pack8_bf16(x);
-    }
   }
+}
+
+// Tokens per block: one while blocks are few (latency), up to eight once there are several waves.
+int tokens_per_block(int tokens) {
+  const int waves = tokens / (8 * sm_count());
+  return waves < 1 ? 1 : waves < kMaxTokens ? waves : kMaxTokens;
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t st) {
-  const int lanes = (p.q_heads + 2 * p.c.kv_heads) * (d / 8);
+  const int n = tokens_per_block(p.b.tokens), blocks = (p.b.tokens + n - 1) / n;
+  const int lanes = (p.q_heads + 2 * p.c.kv_heads) * (d / 8) * n;
   const int passes = (lanes + 255) / 256;
   const int threads = ((lanes + passes - 1) / passes + 31) / 32 * 32;  // whole warps, even passes
-  if (d == 128) (fmt ? kv_append_kernel<128, true> : kv_append_kernel<128, false>)<<<p.b.tokens, threads, 0, st>>>(p);
-  else (fmt ? kv_append_kernel<64, true> : kv_append_kernel<64, false>)<<<p.b.tokens, threads, 0, st>>>(p);
+  if (d == 128) (fmt ? kv_append_kernel<128, true> : kv_append_kernel<128, false>)<<<blocks, threads, 0, st>>>(p, n);
+  else (fmt ? kv_append_kernel<64, true> : kv_append_kernel<64, false>)<<<blocks, threads, 0, st>>>(p, n);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const ReadParams &p, int d, int fmt, cudaStream_t st) {
-  const int lanes = 2 * p.c.kv_heads * (d / 8);
+  const int n = tokens_per_block(p.b.tokens), blocks = (p.b.tokens + n - 1) / n;
+  const int lanes = 2 * p.c.kv_heads * (d / 8) * n;
   const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
-  if (d == 128) (fmt ? kv_read_kernel<128, true> : kv_read_kernel<128, false>)<<<p.b.tokens, threads, 0, st>>>(p);
-  else (fmt ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)<<<p.b.tokens, threads, 0, st>>>(p);
+  if (d == 128) (fmt ? kv_read_kernel<128, true> : kv_read_kernel<128, false>)<<<blocks, threads, 0, st>>>(p, n);
+  else (fmt ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)<<<blocks, threads, 0, st>>>(p, n);
   return cudaGetLastError();
 }
 

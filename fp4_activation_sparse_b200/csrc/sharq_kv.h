@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace sharq {
 
 // ---------------------------------------------------------------- the cache's bytes
@@ -89,6 +91,22 @@ struct NormResidualParams {
   uint16_t *residual_out, *h_out;
   float alpha, eps;
   int tokens, k, rows_per_gate;
+};
+
+// A kernel's dynamic shared-memory limit, set once per device (1 us of every launch otherwise).
+struct SmemOnce {
+  std::atomic<uint64_t> devices{0};
+  template <class Kernel>
+  cudaError_t set(Kernel kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (devices.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
 };
 
 cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t st);

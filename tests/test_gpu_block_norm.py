@@ -63,6 +63,24 @@ def test_zero_and_special_rows():
     assert torch.isfinite(h).all()
 
 
+@pytest.mark.parametrize("size", [6e18, 1e-18])
+def test_rows_whose_squares_leave_float32(size):
+    """Eight squares together overflow or lose float32's precision, their mean over the row does not."""
+    S = require_gpu()
+    rng = np.random.default_rng(7)
+    y, yv = bf16(rng, 3, 4096, scale=size)
+    z = torch.zeros_like(y)
+    y[:, 64:4096 if size > 1 else 64] = 0  # few large values; every small one
+    one = torch.ones(4096, dtype=torch.bfloat16, device="cuda")
+    got = y.double().cpu().numpy()
+    want = got * K.rstd(got, 0.0)
+    for r, h in (S.sharq_norm_residual(y, z, pre_gamma=one, eps=0.0), S.sharq_norm_residual(z, y, pre_gamma=one, eps=0.0)):
+        assert torch.equal(r, y)
+        assert (np.abs(h.double().cpu().numpy() - want) <= np.abs(want) * (BF16 + 2.0 ** -21)).all()
+    r, _ = S.sharq_norm_residual(y, z, post_gamma=one, eps=0.0)
+    assert (np.abs(r.double().cpu().numpy() - want) <= np.abs(want) * (BF16 + 2.0 ** -21)).all()
+
+
 def test_other_stream_and_no_rows():
     S = require_gpu()
     rng = np.random.default_rng(2)
