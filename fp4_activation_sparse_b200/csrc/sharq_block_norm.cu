@@ -11,6 +11,7 @@
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
 #include "sharq_kv.h"
+#include "sharq_kv_device.cuh"
 
 namespace sharq {
 namespace {
@@ -19,20 +20,6 @@ __device__ __forceinline__ uint4 ld128(const void *p) {
   uint4 v;
   asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
-}
-
-// The sum of a unit's eight squares (exact products, seven float32 additions: 4e-7 of it at most) as
-// float64, in which everything further is summed. Where float32 could overflow or underflow the
-// squares are added in float64 one by one.
-__device__ __forceinline__ double sum_squares(const uint4 &v) {
-  float s = bf16lo(v.x) * bf16lo(v.x);
-  s = fmaf(bf16hi(v.x), bf16hi(v.x), s);
-  s = fmaf(bf16lo(v.y), bf16lo(v.y), s), s = fmaf(bf16hi(v.y), bf16hi(v.y), s);
-  s = fmaf(bf16lo(v.z), bf16lo(v.z), s), s = fmaf(bf16hi(v.z), bf16hi(v.z), s);
-  s = fmaf(bf16lo(v.w), bf16lo(v.w), s), s = fmaf(bf16hi(v.w), bf16hi(v.w), s);
-  if (s > 1e30f || s < 1e-25f)
-    return add_squares_exact(v.x, add_squares_exact(v.y, add_squares_exact(v.z, add_squares_exact(v.w, 0.0))));
-  return (double)s;
 }
 
 // rstd of a row from every thread's sum; every warp adds the warps' sums itself, so one barrier is

@@ -3,6 +3,7 @@
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
 #include "sharq_kv.h"
+#include "sharq_kv_device.cuh"
 
 namespace sharq {
 namespace {
@@ -29,17 +30,20 @@ __device__ __forceinline__ uint4 pack8_bf16(const float (&v)[8]) {
   return o;
 }
 
-// Where a token row of the call lives: its position in its sequence, and the row of the cache.
+// Where a token row of the call lives: its position in its sequence, and its row of the cache.
 struct TokenPlace {
-  int pos;            // may be negative (fewer cached than new tokens)
-  int in_use;         // a row of some sequence (rows past the last sequence are not)
-  long long page;     // -1: no place in the cache
+  long long group;           // byte of its group of 16 tokens for key head 0; -1: no place in the cache
+  int codes[2], scales[2];   // its row's first K and V code and scale byte inside a group
+  int pos;                   // may be negative (fewer cached than new tokens)
+  int in_use;                // a row of some sequence (rows past the last sequence are not)
 };
 
 // The places of `n` consecutive tokens. The block counts the sequences that end at or before the
 // first (one pass over cu_q, not a chain of dependent loads); a thread per token searches on.
 constexpr int kMaxTokens = 8;
+template <int D, bool MX>
 __device__ __forceinline__ void find_tokens(const KvBatchView &b, const KvCacheView &c, int token0, int n, TokenPlace *out) {
+  constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
   int seq = 0;
   for (int i0 = 0; i0 < b.n_seq; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
@@ -53,14 +57,18 @@ __device__ __forceinline__ void find_tokens(const KvBatchView &b, const KvCacheV
       if (__ldg(b.cu_q + mid + 1) <= token) seq = mid + 1;
       else hi = mid;
     }
-    TokenPlace t{0, 0, -1};
+    TokenPlace t{-1, {0, 0}, {0, 0}, 0, 0};
     if (seq < b.n_seq && token >= __ldg(b.cu_q)) {
       t.in_use = 1;
       t.pos = __ldg(b.kv_len + seq) - __ldg(b.cu_q + seq + 1) + token;
       const int col = t.pos >> c.page_shift;
       if (t.pos >= 0 && col < b.max_pages) {
         const int page = __ldg(b.page_table + (size_t)seq * b.max_pages + col);
-        if (page >= 0 && page < c.num_pages) t.page = page;
+        const int in_page = t.pos & ((1 << c.page_shift) - 1), r = in_page & 15;
+        if (page >= 0 && page < c.num_pages)
+          t.group = ((((long long)page * c.kv_heads) << (c.page_shift - 4)) + (in_page >> 4)) * G.bytes;
+        t.codes[0] = r * (D / 2), t.codes[1] = G.v_codes + kv_v_place(D, r, 0);
+        t.scales[0] = G.k_scales + r * (D / (MX ? 32 : 16)), t.scales[1] = G.v_scales + kv_v_scale_place(r, 0);
       }
     }
     out[threadIdx.x] = t;
@@ -68,191 +76,203 @@ __device__ __forceinline__ void find_tokens(const KvBatchView &b, const KvCacheV
   __syncthreads();
 }
 
-// Append: a block per one to eight tokens, D/8 lanes per head, eight elements per lane; the lane of
-// the rotation's partner elements loads them itself (they are in L1), so no lane waits for another
-// except for the block maxima. cos and sin are formed once per token from the 64-bit angle and
-// rounded once. Bound by the bytes of the row (read once, q written once); several tokens per block
-// share the latency of finding their places and of the sines.
+// What a lane adds to its token's place: element 8 j of a head.
 template <int D, bool MX>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p, int per_block) {
+struct LanePlace {
+  long long head;  // byte of the key head
+  int codes, scale, is_v;
+  __device__ __forceinline__ LanePlace(const KvCacheView &c, int kh, int v, int j) : is_v(v) {
+    constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
+    const int run = 8 * j / (D / 8), blk = 8 * j / (MX ? 32 : 16);
+    head = ((long long)kh << (c.page_shift - 4)) * G.bytes;
+    codes = v ? kv_v_place(D, 0, run) + (D == 128 ? 4 * (j & 1) : 0) : 4 * j;
+    scale = v ? kv_v_scale_place(0, blk) : blk;
+  }
+};
+
+// Append: a block per one to eight tokens; D/8 lanes per head, eight elements per lane, a lane keeping
+// its head from token to token. The lane of the rotation's partner elements loads them itself (they
+// are in L1), so no lane waits for another except for the block maxima. cos and sin are formed once
+// per token from the 64-bit angle and rounded once. Bound by instructions near the rate of the
+// bytes (the row read once, q and the codes written once); several tokens per block share the
+// latency of finding their places and of the sines.
+template <int D, bool MX>
+__global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p, int per_block) {
   constexpr int L = D / 8;  // lanes per head
-  constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
-  constexpr int NB = D / (MX ? 32 : 16);
-  __shared__ float2 turns[kMaxTokens][D / 2];
+  // cos and sin of angle f of a token at pair_place(f): the lanes of one load read neighbouring words
+  constexpr int NC = D / 16;
+  auto pair_place = [](int f) { return ((f & 7) >> 1) * (2 * NC) + (f >> 3) * 2 + (f & 1); };
+  __shared__ __align__(16) float2 turns[kMaxTokens][D / 2];
   __shared__ TokenPlace places[kMaxTokens];
   const int token0 = blockIdx.x * per_block, n = min(per_block, p.b.tokens - token0);
-  find_tokens(p.b, p.c, token0, n, places);
+  find_tokens<D, MX>(p.b, p.c, token0, n, places);
   for (int i = threadIdx.x; i < n * p.rot_half; i += blockDim.x) {
     const int x = i / p.rot_half, j = i - x * p.rot_half;
     double s, c;
     sincos((double)places[x].pos * (double)__ldg(p.inv_freq + j), &s, &c);
-    turns[x][j] = make_float2(__double2float_rn(c), __double2float_rn(s));
+    turns[x][pair_place(j)] = make_float2(__double2float_rn(c), __double2float_rn(s));
   }
   __syncthreads();
   const int kvh = p.c.kv_heads, heads = p.q_heads + 2 * kvh;
   const int j = threadIdx.x % L, e0 = 8 * j;
-  // whole warps stay in the loop: the shuffles below name every lane
-#pragma unroll 2
-  for (int i0 = 0; i0 < n * heads; i0 += blockDim.x / L) {
-    const int i = i0 + threadIdx.x / L, x_tok = i / heads, head = i - x_tok * heads, token = token0 + x_tok;
-    const TokenPlace tp = places[min(x_tok, n - 1)];
-    const bool live = i < n * heads && tp.in_use;
-    const uint16_t *row = p.qkv + (size_t)token * p.row_stride;
-    const float2 *turn = turns[min(x_tok, n - 1)];
-    const bool is_q = live && head < p.q_heads, is_k = live && !is_q && head < p.q_heads + kvh;
-    float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live) w = ld128(row + (size_t)head * D + e0);
-    const bool turned = (is_q || is_k) && e0 < 2 * p.rot_half;
-    const int partner = p.interleaved ? e0 : e0 < p.rot_half ? e0 + p.rot_half : e0 - p.rot_half;
-    uint4 wp = w;
-    if (turned && !p.interleaved) wp = ld128(row + (size_t)head * D + partner);
-    unpack8(w, x);
-    const uint16_t *gamma = is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr;
-    if (p.q_gamma || p.k_gamma) {  // block-uniform
-      double ss = 0.0;
-      ss = add_squares_exact(w.x, ss), ss = add_squares_exact(w.y, ss);
-      ss = add_squares_exact(w.z, ss), ss = add_squares_exact(w.w, ss);
+  // whole warps stay in the loops: the shuffles below name every lane
+  for (int h0 = 0; h0 < heads; h0 += blockDim.x / L) {
+    const int head = h0 + threadIdx.x / L;
+    const bool live = head < heads, is_q = head < p.q_heads, is_k = !is_q && head < p.q_heads + kvh;
+    const int kh = is_q || !live ? 0 : head - p.q_heads - (is_k ? 0 : kvh);
+    const LanePlace<D, MX> lp(p.c, kh, is_k ? 0 : 1, j);
+    const bool turned = live && (is_q || is_k) && e0 < 2 * p.rot_half;
+    const bool first = e0 < p.rot_half;
+    const int partner = p.interleaved || !turned ? e0 : first ? e0 + p.rot_half : e0 - p.rot_half;
+    const int f0 = p.interleaved ? e0 / 2 : first ? e0 : e0 - p.rot_half;
+    const uint16_t *gamma = !live ? nullptr : is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr;
+    uint4 gw = make_uint4(0, 0, 0, 0), gwp = gw;
+    if (gamma) gw = ld128(gamma + e0), gwp = ld128(gamma + partner);
+    const float *sp = is_k ? p.c.k_scale : p.c.v_scale;
+    const float s = MX || !sp ? 1.f : __ldg(sp + kh), gain = __fdiv_rn(1.f, __fmul_rn(6.f, s));
+    const uint16_t *row = p.qkv + (size_t)token0 * p.row_stride + (size_t)head * D;
+    uint4 w = make_uint4(0, 0, 0, 0), wp = w;
+    auto fetch = [&](int x) {
+      if (!live) return;
+      w = ld128(row + x * p.row_stride + e0);
+      wp = w;
+      if (turned && !p.interleaved) {
+        wp = ld128(row + x * p.row_stride + partner);
+        if (first) wp.x ^= 0x80008000u, wp.y ^= 0x80008000u, wp.z ^= 0x80008000u, wp.w ^= 0x80008000u;  // x1 c - x2 s
+      }
+    };
+    fetch(0);
+    for (int x = 0; x < n; ++x) {
+      const uint4 cur = w, cur_p = wp;
+      if (x + 1 < n) fetch(x + 1);
+      float v[8], y[8];
+      unpack8(cur, v);
+      unpack8(cur_p, y);
+      if (p.q_gamma || p.k_gamma) {  // block-uniform
+        float ss = 0.f;  // of values times 2^-8: the sum of D squares overflows no sooner than their mean
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      const float mean = __double2float_rn(ss * (1.0 / D));
-      const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, p.eps)));
-      unpack8(wp, y);
-      if (gamma) {
-        float g[8], gp[8];
-        unpack8(ld128(gamma + e0), g);
-        unpack8(ld128(gamma + partner), gp);
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i] * 0.00390625f, v[i], ss);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = __fmul_rn(__fmul_rn(x[i], rstd), g[i]);
-          y[i] = __fmul_rn(__fmul_rn(y[i], rstd), gp[i]);
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        const float mean = ss * (256.f / D);
+        const float rstd = __frsqrt_rn(__fadd_rn(mean, p.eps));
+        if (gamma) {
+          float g[8], gp[8];
+          unpack8(gw, g);
+          unpack8(gwp, gp);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] = __fmul_rn(__fmul_rn(v[i], rstd), g[i]);
+            y[i] = __fmul_rn(__fmul_rn(y[i], rstd), gp[i]);
+          }
         }
       }
-    } else {
-      unpack8(wp, y);
-    }
-    if (turned) {
-      float r[8];
-      if (p.interleaved) {
+      if (turned) {
+        const float2 *turn = turns[x] + pair_place(f0);  // two angles are neighbours, the next two 2 NC on
+        if (p.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 cs = turn[e0 / 2 + i];
-          r[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], cs.x), __fmul_rn(x[2 * i + 1], cs.y));
-          r[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], cs.x), __fmul_rn(x[2 * i], cs.y));
+          for (int i = 0; i < 4; ++i) {
+            const float2 cs = turn[(i >> 1) * 2 * NC + (i & 1)];
+            const float a = v[2 * i], b = v[2 * i + 1];
+            v[2 * i] = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+            v[2 * i + 1] = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 cs = turn[(i >> 1) * 2 * NC + (i & 1)];
+            v[i] = __fadd_rn(__fmul_rn(v[i], cs.x), __fmul_rn(y[i], cs.y));
+          }
         }
+      }
+      const TokenPlace &tp = places[x];
+      if (is_q && tp.in_use)
+        *reinterpret_cast<uint4 *>(p.q_out + ((size_t)(token0 + x) * p.q_heads + head) * D + e0) = pack8_bf16(v);
+      if (__all_sync(0xFFFFFFFFu, is_q || !live)) continue;
+      // FP4 codes of the lane's eight elements; the block maximum spans two (four) lanes
+      float am = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) am = max3abs(am, v[i], v[i + 1]);
+      am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+      if (MX) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      if (is_q || !live || !tp.in_use || tp.group < 0) continue;
+      uint32_t sb;
+      float inv;
+      if (MX) {
+        const int e = (int)(__float_as_uint(am) >> 23) - 2;
+        sb = (uint32_t)min(max(e, kKvExpMin), kKvExpMax);
+        inv = __uint_as_float((254u - sb) << 23);
       } else {
-        const bool first = e0 < p.rot_half;
-        const int f0 = first ? e0 : e0 - p.rot_half;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 cs = turn[f0 + i];
-          const float a = __fmul_rn(x[i], cs.x), b = __fmul_rn(y[i], cs.y);
-          r[i] = first ? __fsub_rn(a, b) : __fadd_rn(a, b);
-        }
+        sb = cvt_e4m3(__fmul_rn(am, gain));
+        const float d = __fmul_rn(e4m3_to_f32(sb), s);
+        inv = d == 0.f ? 0.f : __frcp_rn(d);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = r[i];
-    }
-    if (is_q) *reinterpret_cast<uint4 *>(p.q_out + ((size_t)token * p.q_heads + head) * D + e0) = pack8_bf16(x);
-    // FP4 codes of the lane's eight elements; the block maximum spans two (four) lanes
-    float am = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i]));
-    am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    if (MX) am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    if (is_q || !live || tp.page < 0) continue;
-    const int kh = is_k ? head - p.q_heads : head - p.q_heads - kvh;
-    uint32_t sb;
-    float inv;
-    if (MX) {
-      const int e = (int)(__float_as_uint(am) >> 23) - 2;
-      sb = (uint32_t)min(max(e, kKvExpMin), kKvExpMax);
-      inv = __uint_as_float((254u - sb) << 23);
-    } else {
-      const float *sp = is_k ? p.c.k_scale : p.c.v_scale;
-      const float s = sp ? __ldg(sp + kh) : 1.f;
-      sb = cvt_e4m3(__fmul_rn(am, __fdiv_rn(1.f, __fmul_rn(6.f, s))));
-      const float d = __fmul_rn(e4m3_to_f32(sb), s);
-      inv = d == 0.f ? 0.f : __frcp_rn(d);
-    }
-    const uint32_t codes = cvt_e2m1x8(__fmul_rn(x[0], inv), __fmul_rn(x[1], inv), __fmul_rn(x[2], inv),
-                                      __fmul_rn(x[3], inv), __fmul_rn(x[4], inv), __fmul_rn(x[5], inv),
-                                      __fmul_rn(x[6], inv), __fmul_rn(x[7], inv));
-    const int in_page = tp.pos & ((1 << p.c.page_shift) - 1), r = in_page & 15;
-    uint8_t *grp = p.c.pages + ((((size_t)tp.page * kvh + kh) << (p.c.page_shift - 4)) + (in_page >> 4)) * G.bytes;
-    const int blk = e0 / (MX ? 32 : 16);
-    const bool writes_scale = e0 % (MX ? 32 : 16) == 0;
-    if (is_k) {
-      *reinterpret_cast<uint32_t *>(grp + r * (D / 2) + 4 * j) = codes;
-      if (writes_scale) grp[G.k_scales + r * NB + blk] = (uint8_t)sb;
-    } else {
-      *reinterpret_cast<uint32_t *>(grp + G.v_codes + kv_v_place(D, r, e0 / (D / 8)) + (D == 128 ? 4 * (j & 1) : 0)) = codes;
-      if (writes_scale) grp[G.v_scales + kv_v_scale_place(r, blk)] = (uint8_t)sb;
+      uint8_t *grp = p.c.pages + tp.group + lp.head;
+      *reinterpret_cast<uint32_t *>(grp + tp.codes[lp.is_v] + lp.codes) =
+          cvt_e2m1x8(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv), __fmul_rn(v[2], inv), __fmul_rn(v[3], inv),
+                     __fmul_rn(v[4], inv), __fmul_rn(v[5], inv), __fmul_rn(v[6], inv), __fmul_rn(v[7], inv));
+      if (e0 % (MX ? 32 : 16) == 0) grp[tp.scales[lp.is_v] + lp.scale] = (uint8_t)sb;
     }
   }
 }
 
-// Read: a block per one to eight tokens; a lane turns eight codes and their scale into values, four
-// such units in flight at once.
+// Read: a block per one to eight tokens; a lane turns eight codes and their scale into values, the
+// same eight elements of four tokens at a time. code * block scale is exact in float16.
 template <int D, bool MX>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams p, int per_block) {
   constexpr int L = D / 8, U = 4;
-  constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
-  constexpr int NB = D / (MX ? 32 : 16);
   __shared__ TokenPlace places[kMaxTokens];
   const int token0 = blockIdx.x * per_block, n = min(per_block, p.b.tokens - token0);
-  find_tokens(p.b, p.c, token0, n, places);
-  const int kvh = p.c.kv_heads, units = 2 * kvh * L;
-  for (int i0 = threadIdx.x; i0 < n * units; i0 += U * blockDim.x) {
-    uint32_t codes[U], sb[U];
+  find_tokens<D, MX>(p.b, p.c, token0, n, places);
+  const int kvh = p.c.kv_heads;
+  for (int in = threadIdx.x; in < 2 * kvh * L; in += blockDim.x) {
+    const int j = in % L, is_v = in >= kvh * L, kh = in / L - is_v * kvh;
+    const LanePlace<D, MX> lp(p.c, kh, is_v, j);
+    const float *sp = is_v ? p.c.v_scale : p.c.k_scale;
+    const float s = MX || !sp ? 1.f : __ldg(sp + kh);
+    const size_t o0 = ((size_t)token0 * kvh + kh) * D + 8 * j, step = (size_t)kvh * D;
+    void *out = is_v ? p.v_out : p.k_out;
+    for (int x0 = 0; x0 < n; x0 += U) {
+      uint32_t codes[U], sb[U];
 #pragma unroll
-    for (int y = 0; y < U; ++y) {
-      const int i = i0 + y * blockDim.x;
-      codes[y] = sb[y] = 0u;
-      if (i >= n * units) continue;
-      const int x = i / units, in = i - x * units, j = in % L, is_v = in >= kvh * L, head = in / L - is_v * kvh, e0 = 8 * j;
-      const TokenPlace tp = places[x];
-      if (tp.page < 0) continue;
-      const int in_page = tp.pos & ((1 << p.c.page_shift) - 1), r = in_page & 15, blk = e0 / (MX ? 32 : 16);
-      const uint8_t *grp =
-          p.c.pages + ((((size_t)tp.page * kvh + head) << (p.c.page_shift - 4)) + (in_page >> 4)) * G.bytes;
-      const int at = is_v ? G.v_codes + kv_v_place(D, r, e0 / (D / 8)) + (D == 128 ? 4 * (j & 1) : 0) : r * (D / 2) + 4 * j;
-      codes[y] = *reinterpret_cast<const uint32_t *>(grp + at);
-      sb[y] = grp[is_v ? G.v_scales + kv_v_scale_place(r, blk) : G.k_scales + r * NB + blk];
-    }
-#pragma unroll
-    for (int y = 0; y < U; ++y) {
-      const int i = i0 + y * blockDim.x;
-      if (i >= n * units) continue;
-      const int x = i / units, in = i - x * units, j = in % L, is_v = in >= kvh * L, head = in / L - is_v * kvh, e0 = 8 * j;
-      if (!places[x].in_use) continue;
-      const float *sp = is_v ? p.c.v_scale : p.c.k_scale;
-      const float s = MX ? 1.f : sp ? __ldg(sp + head) : 1.f, b = MX ? e8m0_to_f32(sb[y]) : e4m3_to_f32(sb[y]);
-      uint32_t h[4];
-      cvt_e2m1x8_to_f16x2(codes[y], h);
-      float v[8];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 f = half2_bits_to_float2(h[q]);
-        v[2 * q] = __fmul_rn(__fmul_rn(f.x, b), s);
-        v[2 * q + 1] = __fmul_rn(__fmul_rn(f.y, b), s);
+      for (int y = 0; y < U; ++y) {
+        codes[y] = sb[y] = 0u;
+        if (x0 + y < n && places[x0 + y].group >= 0) {
+          const TokenPlace &tp = places[x0 + y];
+          const uint8_t *grp = p.c.pages + tp.group + lp.head;
+          codes[y] = *reinterpret_cast<const uint32_t *>(grp + tp.codes[is_v] + lp.codes);
+          sb[y] = grp[tp.scales[is_v] + lp.scale];
+        }
       }
-      const size_t o = ((size_t)(token0 + x) * kvh + head) * D + e0;
-      void *out = is_v ? p.v_out : p.k_out;
-      if (p.out_f32) {
-        float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
-        f[0] = make_float4(v[0], v[1], v[2], v[3]);
-        f[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + o) = pack8_bf16(v);
+#pragma unroll
+      for (int y = 0; y < U; ++y) {
+        if (x0 + y >= n || !places[x0 + y].in_use) continue;
+        const uint32_t b = kv_scales2<MX>(sb[y] * 0x101u);
+        uint32_t h[4];
+        cvt_e2m1x8_to_f16x2(codes[y], h);
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = half2_bits_to_float2(mul2(h[q], b));
+          v[2 * q] = __fmul_rn(f.x, s), v[2 * q + 1] = __fmul_rn(f.y, s);
+        }
+        const size_t o = o0 + (x0 + y) * step;
+        if (p.out_f32) {
+          float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
+          f[0] = make_float4(v[0], v[1], v[2], v[3]);
+          f[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + o) = pack8_bf16(v);
+        }
       }
     }
   }
 }
 
+constexpr int kTokenBlocks = 16;
 // Tokens per block: one while blocks are few (latency), up to eight once there are several waves.
 int tokens_per_block(int tokens) {
-  const int waves = tokens / (8 * sm_count());
+  const int waves = tokens / (kTokenBlocks * sm_count());
   return waves < 1 ? 1 : waves < kMaxTokens ? waves : kMaxTokens;
 }
 
@@ -260,7 +280,7 @@ int tokens_per_block(int tokens) {
 
 cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t st) {
   const int n = tokens_per_block(p.b.tokens), blocks = (p.b.tokens + n - 1) / n;
-  const int lanes = (p.q_heads + 2 * p.c.kv_heads) * (d / 8) * n;
+  const int lanes = (p.q_heads + 2 * p.c.kv_heads) * (d / 8);
   const int passes = (lanes + 255) / 256;
   const int threads = ((lanes + passes - 1) / passes + 31) / 32 * 32;  // whole warps, even passes
   if (d == 128) (fmt ? kv_append_kernel<128, true> : kv_append_kernel<128, false>)<<<blocks, threads, 0, st>>>(p, n);
@@ -270,7 +290,7 @@ cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t
 
 cudaError_t launch_kv_read(const ReadParams &p, int d, int fmt, cudaStream_t st) {
   const int n = tokens_per_block(p.b.tokens), blocks = (p.b.tokens + n - 1) / n;
-  const int lanes = 2 * p.c.kv_heads * (d / 8) * n;
+  const int lanes = 2 * p.c.kv_heads * (d / 8);
   const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
   if (d == 128) (fmt ? kv_read_kernel<128, true> : kv_read_kernel<128, false>)<<<blocks, threads, 0, st>>>(p, n);
   else (fmt ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)<<<blocks, threads, 0, st>>>(p, n);

@@ -1,4 +1,4 @@
-// Device helpers shared by the attention kernels over the FP4 cache.
+// Device helpers shared by the kernels of the attention side.
 #pragma once
 
 #include "sharq_common.cuh"
@@ -53,6 +53,20 @@ __device__ __forceinline__ uint32_t kv_scales2(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
   }
   return d;
+}
+
+// The sum of a unit's eight squares (exact products, seven float32 additions: 4e-7 of it at most) as
+// float64, in which everything further is summed. Where float32 could overflow or underflow the
+// squares are added in float64 one by one.
+__device__ __forceinline__ double sum_squares(const uint4 &v) {
+  float s = bf16lo(v.x) * bf16lo(v.x);
+  s = fmaf(bf16hi(v.x), bf16hi(v.x), s);
+  s = fmaf(bf16lo(v.y), bf16lo(v.y), s), s = fmaf(bf16hi(v.y), bf16hi(v.y), s);
+  s = fmaf(bf16lo(v.z), bf16lo(v.z), s), s = fmaf(bf16hi(v.z), bf16hi(v.z), s);
+  s = fmaf(bf16lo(v.w), bf16lo(v.w), s), s = fmaf(bf16hi(v.w), bf16hi(v.w), s);
+  if (s > 1e30f || s < 1e-25f)
+    return add_squares_exact(v.x, add_squares_exact(v.y, add_squares_exact(v.z, add_squares_exact(v.w, 0.0))));
+  return (double)s;
 }
 
 // row / group for row < 2^32 / group (the entry point keeps to that)
