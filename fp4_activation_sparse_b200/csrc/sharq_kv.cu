@@ -91,8 +91,7 @@ struct LanePlace {
 };
 
 // Append: a block per one to eight tokens; D/8 lanes per head, eight elements per lane, a lane keeping
-// its head from token to token. The lane of the rotation's partner elements loads them itself (they
-// are in L1), so no lane waits for another except for the block maxima. cos and sin are formed once
+// its head from token to token; partner elements and block maxima come by shuffles. cos and sin are formed once
 // per token from the 64-bit angle and rounded once. Bound by instructions near the rate of the
 // bytes (the row read once, q and the codes written once); several tokens per block share the
 // latency of finding their places and of the sines.
@@ -105,6 +104,17 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
   __shared__ __align__(16) float2 turns[kMaxTokens][D / 2];
   __shared__ TokenPlace places[kMaxTokens];
   const int token0 = blockIdx.x * per_block, n = min(per_block, p.b.tokens - token0);
+  const int kvh = p.c.kv_heads, heads = p.q_heads + 2 * kvh, at_once = blockDim.x / L;
+  const int j = threadIdx.x % L, e0 = 8 * j;
+  // the rows of two iterations ahead are on their way, the first while the places and sines are found
+  int next_head = threadIdx.x / L, next_x = 0;
+  auto fetch = [&]() {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (next_head < heads) w = ld128(p.qkv + (size_t)(token0 + next_x) * p.row_stride + (size_t)next_head * D + e0);
+    if (++next_x == n) next_x = 0, next_head += at_once;
+    return w;
+  };
+  uint4 ahead1 = fetch(), ahead2 = fetch();
   find_tokens<D, MX>(p.b, p.c, token0, n, places);
   for (int i = threadIdx.x; i < n * p.rot_half; i += blockDim.x) {
     const int x = i / p.rot_half, j = i - x * p.rot_half;
@@ -113,10 +123,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
     turns[x][pair_place(j)] = make_float2(__double2float_rn(c), __double2float_rn(s));
   }
   __syncthreads();
-  const int kvh = p.c.kv_heads, heads = p.q_heads + 2 * kvh;
-  const int j = threadIdx.x % L, e0 = 8 * j;
   // whole warps stay in the loops: the shuffles below name every lane
-  for (int h0 = 0; h0 < heads; h0 += blockDim.x / L) {
+  for (int h0 = 0; h0 < heads; h0 += at_once) {
     const int head = h0 + threadIdx.x / L;
     const bool live = head < heads, is_q = head < p.q_heads, is_k = !is_q && head < p.q_heads + kvh;
     const int kh = is_q || !live ? 0 : head - p.q_heads - (is_k ? 0 : kvh);
@@ -130,21 +138,15 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
     if (gamma) gw = ld128(gamma + e0), gwp = ld128(gamma + partner);
     const float *sp = is_k ? p.c.k_scale : p.c.v_scale;
     const float s = MX || !sp ? 1.f : __ldg(sp + kh), gain = __fdiv_rn(1.f, __fmul_rn(6.f, s));
-    const uint16_t *row = p.qkv + (size_t)token0 * p.row_stride + (size_t)head * D;
-    uint4 w = make_uint4(0, 0, 0, 0), wp = w;
-    auto fetch = [&](int x) {
-      if (!live) return;
-      w = ld128(row + x * p.row_stride + e0);
-      wp = w;
-      if (turned && !p.interleaved) {
-        wp = ld128(row + x * p.row_stride + partner);
-        if (first) wp.x ^= 0x80008000u, wp.y ^= 0x80008000u, wp.z ^= 0x80008000u, wp.w ^= 0x80008000u;  // x1 c - x2 s
-      }
-    };
-    fetch(0);
+    const int partner_lane = (threadIdx.x & 31) + (partner - e0) / 8;
+    const uint32_t flip = turned && !p.interleaved && first ? 0x80008000u : 0u;  // x1 c - x2 s
     for (int x = 0; x < n; ++x) {
-      const uint4 cur = w, cur_p = wp;
-      if (x + 1 < n) fetch(x + 1);
+      const uint4 cur = ahead1;
+      ahead1 = ahead2;
+      ahead2 = fetch();
+      uint4 cur_p;
+      cur_p.x = __shfl_sync(0xFFFFFFFFu, cur.x, partner_lane) ^ flip, cur_p.y = __shfl_sync(0xFFFFFFFFu, cur.y, partner_lane) ^ flip;
+      cur_p.z = __shfl_sync(0xFFFFFFFFu, cur.z, partner_lane) ^ flip, cur_p.w = __shfl_sync(0xFFFFFFFFu, cur.w, partner_lane) ^ flip;
       float v[8], y[8];
       unpack8(cur, v);
       unpack8(cur_p, y);
