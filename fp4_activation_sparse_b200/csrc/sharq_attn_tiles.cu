@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
   __shared__ Work ring[2];
   __shared__ long long warp_sums[kThreads / 32];
   __shared__ float row_coef[2 * kRows];  // score factor of each row of the segment
+  __shared__ float2 row_join[2][kRows];
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t last_part[2];
   __shared__ volatile uint32_t abort_flag;
@@ -670,27 +671,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
       if (!last_part[t]) continue;
       __threadfence();
-      if (!live) continue;
-      float mm = -INFINITY, ll = 0.f;
-      for (int j = 0; j < w.parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
-      const float ref = mm == -INFINITY ? 0.f : mm;
-      for (int j = 0; j < w.parts.count; ++j)
-        ll += __ldcg(part_at(j) + (D + 1) * kRows) * kv_ex2(__ldcg(part_at(j) + D * kRows) - ref);
-      const float inv_all = ll == 0.f ? 0.f : v_scale / ll;
-#pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
-        float o[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0.f;
-        for (int j = 0; j < w.parts.count; ++j) {
-          const float *src = part_at(j);
-          const float f = kv_ex2(__ldcg(src + D * kRows) - ref);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(src + (32 * x + e) * kRows), f, o[e]);
-        }
-        put(x, o, inv_all);
+      // joined in the order of the keys: a thread finds its row's factor, then the tile's threads share
+      // the live rows' elements eight at a time, so that every part's loads are in flight together
+      const int live_rows = min(w.r.rows - t * kRows, kRows);
+      if (live) {
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < w.parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
+        const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
+        for (int j = 0; j < w.parts.count; ++j)
+          ll += __ldcg(part_at(j) + (D + 1) * kRows) * kv_ex2(__ldcg(part_at(j) + D * kRows) - ref);
+        row_join[t][r] = make_float2(ref, ll == 0.f ? 0.f : v_scale / ll);
+        put_lse(mm, ll);
       }
-      put_lse(mm, ll);
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
+      for (int idx = r; idx < live_rows * (D / 8); idx += kRows) {
+        const int c8 = idx / live_rows, row = idx - c8 * live_rows;
+        const float2 join = row_join[t][row];
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int j = 0; j < w.parts.count; ++j) {
+          const float *src = part_at(j) - r + row;
+          const float f = kv_ex2(__ldcg(src + D * kRows) - join.x) * join.y;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(__ldcg(src + (8 * c8 + e) * kRows), f, o[e]);
+        }
+        const int in_seq = w.r.row0 + t * kRows + row, tok = token_in(p, in_seq);
+        const int to_token = w.r.q0 + tok, to_head = w.kh * p.group + in_seq - tok * p.group;
+        if (to_token < 0 || to_token >= p.b.tokens) continue;
+        uint4 out;
+        uint32_t *ow = &out.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+          ow[e] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p.y + ((size_t)to_token * p.q_heads + to_head) * D + 8 * c8) = out;
+      }
     }
     tc_fence_before();
   } else if (warp < 12) {
