@@ -235,45 +235,50 @@ __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt
 }
 
 // ---------------------------------------------------------------- codes to float16 tiles
-// Two groups of 16 tokens per warp and step, one after the other in a short loop (the code of every
-// role shares the instruction cache). K: a 16-byte unit (32 elements of one row) per lane and load;
-// V: the 16 bytes of lane 4g + t are four (D = 64) or two (D = 128) rows' runs of D/8 elements.
-// Stores are 16 bytes to swizzled rows; the lanes of one store cover every bank group four times,
-// the least that 512 bytes can take.
+// Two groups of 16 tokens per warp and step. K: a 16-byte unit (32 elements of one row) per lane
+// and load; V: the 16 bytes of lane 4g + t are four (D = 64) or two (D = 128) rows' runs of D/8
+// elements. Stores are 16 bytes to swizzled rows; the lanes of one store cover every bank group
+// four times, the least that 512 bytes can take.
 template <int D, bool MX>
 struct Codes {
   static constexpr int U = D / 64;  // 16-byte units per lane, group and operand
-  uint4 u[U];
-  uint32_t s[U];
+  uint4 u[2][U];
+  uint32_t s[2][U];
 };
 
 template <int D, bool MX>
-__device__ __forceinline__ void load_k(const uint8_t *grp, int lane, Codes<D, MX> &c) {
+__device__ __forceinline__ void load_k(const uint8_t *const (&grp)[2], int lane, Codes<D, MX> &c) {
   constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
   constexpr int NB = D / (MX ? 32 : 16), UR = D / 32;  // scales and units per row
 #pragma unroll
-  for (int x = 0; x < D / 64; ++x) {
-    c.u[x] = make_uint4(0, 0, 0, 0);
-    c.s[x] = 0;
-    if (grp) {
-      const int unit = lane + 32 * x;
-      c.u[x] = __ldg(reinterpret_cast<const uint4 *>(grp) + unit);
-      const uint8_t *sp = grp + G.k_scales + (unit / UR) * NB + (unit % UR) * (NB / UR);
-      c.s[x] = MX ? (uint32_t)__ldg(sp) : (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(sp));
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) {
+      c.u[g][x] = make_uint4(0, 0, 0, 0);
+      c.s[g][x] = 0;
+      if (grp[g]) {
+        const int unit = lane + 32 * x;
+        c.u[g][x] = __ldg(reinterpret_cast<const uint4 *>(grp[g]) + unit);
+        const uint8_t *sp = grp[g] + G.k_scales + (unit / UR) * NB + (unit % UR) * (NB / UR);
+        c.s[g][x] = MX ? (uint32_t)__ldg(sp) : (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(sp));
+      }
     }
-  }
 }
 template <int D, bool MX>
-__device__ __forceinline__ void load_v(const uint8_t *grp, int lane, Codes<D, MX> &c) {
+__device__ __forceinline__ void load_v(const uint8_t *const (&grp)[2], int lane, Codes<D, MX> &c) {
   constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
   constexpr int per_run = (MX ? 32 : 16) / (D / 8);  // runs that share a block
 #pragma unroll
-  for (int x = 0; x < D / 64; ++x) {
-    c.u[x] = make_uint4(0, 0, 0, 0);
-    if (grp) c.u[x] = __ldg(reinterpret_cast<const uint4 *>(grp + G.v_codes) + lane + 32 * x);
+  for (int g = 0; g < 2; ++g) {
+#pragma unroll
+    for (int x = 0; x < D / 64; ++x) {
+      c.u[g][x] = make_uint4(0, 0, 0, 0);
+      if (grp[g]) c.u[g][x] = __ldg(reinterpret_cast<const uint4 *>(grp[g] + G.v_codes) + lane + 32 * x);
+    }
+    c.s[g][0] = 0;
+    if (grp[g])
+      c.s[g][0] = __ldg(reinterpret_cast<const uint32_t *>(grp[g] + G.v_scales) + (lane >> 2) / per_run * 4 + (lane & 3));
   }
-  c.s[0] = 0;
-  if (grp) c.s[0] = __ldg(reinterpret_cast<const uint32_t *>(grp + G.v_scales) + (lane >> 2) / per_run * 4 + (lane & 3));
 }
 
 // eight codes times one scale pair -> 16 bytes of float16
@@ -290,40 +295,46 @@ template <int D, bool MX>
 __device__ __forceinline__ void store_k(uint32_t tile, int row0, int lane, const Codes<D, MX> &c) {
   constexpr int UR = D / 32;
 #pragma unroll
-  for (int x = 0; x < D / 64; ++x) {
-    const int unit = lane + 32 * x, row = row0 + unit / UR, chunk = (unit % UR) * 4;
-    const uint32_t two = kv_scales2<MX>(MX ? c.s[x] * 0x101u : c.s[x]);
-    const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
-    const uint32_t *w = &c.u[x].x;
+  for (int g = 0; g < 2; ++g)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put8(tile_addr(tile, row, chunk + i), w[i], i < 2 ? s0 : s1);
-  }
+    for (int x = 0; x < D / 64; ++x) {
+      const int unit = lane + 32 * x, row = row0 + 16 * g + unit / UR, chunk = (unit % UR) * 4;
+      const uint32_t two = kv_scales2<MX>(MX ? c.s[g][x] * 0x101u : c.s[g][x]);
+      const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
+      const uint32_t *w = &c.u[g][x].x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) put8(tile_addr(tile, row, chunk + i), w[i], i < 2 ? s0 : s1);
+    }
 }
-// left: keys of the group that exist (the scales of the others may be anything)
+// left: keys of each group that exist (the scales of the others may be anything)
 template <int D, bool MX>
 __device__ __forceinline__ void store_v(uint32_t tile, int row0, int lane, int left, const Codes<D, MX> &c) {
   const int run = lane >> 2, t = lane & 3;
-  uint32_t s = c.s[0];
-  if (left < 16) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (8 * (q >> 1) + 2 * t + (q & 1) >= left) s &= ~(0xFFu << (8 * q));
-  }
+  for (int g = 0; g < 2; ++g) {
+    uint32_t s = c.s[g][0];
+    if (left < 16 * (g + 1)) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t two = kv_scales2<MX>(h ? s >> 16 : s & 0xFFFFu);
+      for (int q = 0; q < 4; ++q)
+        if (16 * g + 8 * (q >> 1) + 2 * t + (q & 1) >= left) s &= ~(0xFFu << (8 * q));
+    }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t sc = __byte_perm(two, 0, j ? 0x3232 : 0x1010);
-      const int row = row0 + 8 * h + 2 * t + j;
-      const uint4 u = c.u[h % (D / 64)];
-      if (D == 128) {
-        const uint32_t w0 = j ? u.z : u.x, w1 = j ? u.w : u.y;
-        const bool swap = run >= 4;  // half the lanes begin with the upper chunk: every bank group in turn
-        put8(tile_addr(tile, row, 2 * run + (swap ? 1 : 0)), swap ? w1 : w0, sc);
-        put8(tile_addr(tile, row, 2 * run + (swap ? 0 : 1)), swap ? w0 : w1, sc);
-      } else {
-        put8(tile_addr(tile, row, run), h ? (j ? u.w : u.z) : (j ? u.y : u.x), sc);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t two = kv_scales2<MX>(h ? s >> 16 : s & 0xFFFFu);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t sc = __byte_perm(two, 0, j ? 0x3232 : 0x1010);
+        const int row = row0 + 16 * g + 8 * h + 2 * t + j;
+        if (D == 128) {
+          const uint32_t w0 = j ? c.u[g][h % (D / 64)].z : c.u[g][h % (D / 64)].x;
+          const uint32_t w1 = j ? c.u[g][h % (D / 64)].w : c.u[g][h % (D / 64)].y;
+          const bool swap = run >= 4;  // half the lanes begin with the upper chunk: every bank group in turn
+          put8(tile_addr(tile, row, 2 * run + (swap ? 1 : 0)), swap ? w1 : w0, sc);
+          put8(tile_addr(tile, row, 2 * run + (swap ? 0 : 1)), swap ? w0 : w1, sc);
+        } else {
+          const uint4 u = c.u[g][0];
+          put8(tile_addr(tile, row, run), h ? (j ? u.w : u.z) : (j ? u.y : u.x), sc);
+        }
       }
     }
   }
@@ -429,7 +440,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
   __shared__ Work ring[2];
   __shared__ long long warp_sums[kThreads / 32];
   __shared__ float row_coef[2 * kRows];  // score factor of each row of the segment
-  __shared__ float2 row_join[2][kRows];
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t last_part[2];
   __shared__ volatile uint32_t abort_flag;
@@ -660,44 +670,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
       if (!last_part[t]) continue;
       __threadfence();
-      // joined in the order of the keys: a thread finds its row's factor, then the tile's threads share
-      // the live rows' elements eight at a time, so that every part's loads are in flight together
-      const int live_rows = min(w.r.rows - t * kRows, kRows);
-      if (live) {
-        float mm = -INFINITY, ll = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < w.parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
-        const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-        for (int j = 0; j < w.parts.count; ++j)
-          ll += __ldcg(part_at(j) + (D + 1) * kRows) * kv_ex2(__ldcg(part_at(j) + D * kRows) - ref);
-        row_join[t][r] = make_float2(ref, ll == 0.f ? 0.f : v_scale / ll);
-        put_lse(mm, ll);
-      }
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
-      for (int idx = r; idx < live_rows * (D / 8); idx += kRows) {
-        const int c8 = idx / live_rows, row = idx - c8 * live_rows;
-        const float2 join = row_join[t][row];
-        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+      if (!live) continue;
+      float mm = -INFINITY, ll = 0.f;
+      for (int j = 0; j < w.parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      for (int j = 0; j < w.parts.count; ++j)
+        ll += __ldcg(part_at(j) + (D + 1) * kRows) * kv_ex2(__ldcg(part_at(j) + D * kRows) - ref);
+      const float inv_all = ll == 0.f ? 0.f : v_scale / ll;
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        float o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0.f;
         for (int j = 0; j < w.parts.count; ++j) {
-          const float *src = part_at(j) - r + row;
-          const float f = kv_ex2(__ldcg(src + D * kRows) - join.x) * join.y;
+          const float *src = part_at(j);
+          const float f = kv_ex2(__ldcg(src + D * kRows) - ref);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(__ldcg(src + (8 * c8 + e) * kRows), f, o[e]);
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(src + (32 * x + e) * kRows), f, o[e]);
         }
-        const int in_seq = w.r.row0 + t * kRows + row, tok = token_in(p, in_seq);
-        const int to_token = w.r.q0 + tok, to_head = w.kh * p.group + in_seq - tok * p.group;
-        if (to_token < 0 || to_token >= p.b.tokens) continue;
-        uint4 out;
-        uint32_t *ow = &out.x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
-          ow[e] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(p.y + ((size_t)to_token * p.q_heads + to_head) * D + 8 * c8) = out;
+        put(x, o, inv_all);
       }
+      put_lse(mm, ll);
     }
     tc_fence_before();
   } else if (warp < 12) {
@@ -710,56 +703,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       const int begin = ring[seg & 1].r.begin, end = ring[seg & 1].r.end, kv_len = ring[seg & 1].r.kv_len, kh = ring[seg & 1].kh;
       const int *table = p.b.page_table + (size_t)ring[seg & 1].seq * p.b.max_pages;
       done_work(bars, seg);
-      // the warp's q-th group of the segment is group q & 1 of step begin + q / 2
-      auto page_of = [&](int q) -> int {  // its page id; -1: no keys there
-        const int gi = (begin + (q >> 1)) * 8 + 2 * dw + (q & 1), col = gi >> (p.c.page_shift - 4);
-        if (q >= 2 * (end - begin) || 16 * gi >= kv_len || col >= p.b.max_pages) return -1;
+      auto page_of = [&](int i, int g) -> int {  // page id of the warp's group g of step i; -1: no keys there
+        const int gi = i * 8 + 2 * dw + g, col = gi >> (p.c.page_shift - 4);
+        if (i >= end || 16 * gi >= kv_len || col >= p.b.max_pages) return -1;
         const int page = __ldg(table + col);
         return page < p.c.num_pages ? page : -1;
       };
-      auto place = [&](int q, int page) -> const uint8_t * {
+      auto place = [&](int i, int g, int page) -> const uint8_t * {
         if (page < 0) return nullptr;
-        const int gi = (begin + (q >> 1)) * 8 + 2 * dw + (q & 1);
+        const int gi = i * 8 + 2 * dw + g;
         return p.c.pages + ((((size_t)page * p.c.kv_heads + kh) << (p.c.page_shift - 4)) + (gi & group_mask)) * G.bytes;
       };
-      // K runs one step ahead of V, as the products do; one group's codes and the page id of the one
-      // after it are in flight for each
+      // K runs one step ahead of V, as the products do
       Codes<D, MX> ck, cv;
-      int k_page = page_of(0), v_page = k_page, kq = 0, vq = 0;
-      load_k<D, MX>(place(0, k_page), lane, ck);
-      load_v<D, MX>(place(0, v_page), lane, cv);
-      int k_next = page_of(1), v_next = k_next;
+      int next0 = page_of(begin, 0), next1 = page_of(begin, 1);
+      const uint8_t *k_grp[2] = {place(begin, 0, next0), place(begin, 1, next1)};
+      load_k<D, MX>(k_grp, lane, ck);
+      load_v<D, MX>(k_grp, lane, cv);
+      next0 = page_of(begin + 1, 0), next1 = page_of(begin + 1, 1);
       for (int i = begin - 1; i < end; ++i) {
         if (i + 1 < end) {
           const int nk = n + 1 + i - begin, st = nk & 1;
+          const uint32_t bits = (k_grp[0] ? 1u : 0u) | (k_grp[1] ? 2u : 0u);
           if (nk >= 2 && !(ok = mbar_wait(bar(bars.k_empty[st]), ((nk >> 1) - 1) & 1, limit, &abort_flag))) break;
-          uint32_t bits = 0;
-#pragma unroll 1
-          for (int g = 0; g < 2; ++g) {
-            bits |= (k_page >= 0 ? 1u : 0u) << g;
-            store_k<D, MX>(base + M::kK + st * M::kTile, 32 * dw + 16 * g, lane, ck);
-            k_page = k_next;
-            ++kq;
-            load_k<D, MX>(place(kq, k_page), lane, ck);
-            k_next = page_of(kq + 1);
-          }
+          store_k<D, MX>(base + M::kK + st * M::kTile, 32 * dw, lane, ck);
           if (lane == 0) reinterpret_cast<volatile uint8_t *>(&valid[nk % kValidRing])[dw] = (uint8_t)bits;
           fence_proxy_async();
           mbar_arrive_warp(bar(bars.k_full[st]));
         }
+        const uint8_t *v_grp[2] = {k_grp[0], k_grp[1]};
+        k_grp[0] = place(i + 2, 0, next0), k_grp[1] = place(i + 2, 1, next1);
+        next0 = page_of(i + 3, 0), next1 = page_of(i + 3, 1);
+        load_k<D, MX>(k_grp, lane, ck);
         if (i < begin) continue;
         const int nv = n + i - begin, st = nv & 1;
         if (nv >= 2 && !(ok = mbar_wait(bar(bars.v_empty[st]), ((nv >> 1) - 1) & 1, limit, &abort_flag))) break;
-#pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          store_v<D, MX>(base + M::kV + st * M::kTile, 32 * dw + 16 * g, lane, kv_len - (i * kKeys + 32 * dw + 16 * g), cv);
-          v_page = v_next;
-          ++vq;
-          load_v<D, MX>(place(vq, v_page), lane, cv);
-          v_next = page_of(vq + 1);
-        }
+        store_v<D, MX>(base + M::kV + st * M::kTile, 32 * dw, lane, kv_len - (i * kKeys + 32 * dw), cv);
         fence_proxy_async();
         mbar_arrive_warp(bar(bars.v_full[st]));
+        load_v<D, MX>(v_grp, lane, cv);
       }
       n += end - begin;
       ok = __all_sync(0xFFFFFFFFu, ok);
