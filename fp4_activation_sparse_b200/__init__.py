@@ -402,17 +402,19 @@ def _reject(message: str):
     raise SharqError(SHARQ_ERR_INVALID_ARG, message)
 
 
-def _tensor(t, name: str, dtype, device, shape=None, contiguous: bool = True):
-    """Checks one device tensor argument (`shape` entries of None are free)."""
+def _tensor(t, name: str, dtype, device: int | None, shape=None, contiguous: bool = True):
+    """Checks one device tensor argument (`device`: index, `shape`: entries of None are free)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and (not contiguous or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _reject(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         _reject(f"{name} must be {dtype} (got {t.dtype})")
-    if device is not None and t.device != device:
-        _reject(f"{name} is on {t.device}, the call on {device}")
-    if shape is not None and t.shape != shape:
-        if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-            _reject(f"{name} must have shape {tuple('any' if n is None else n for n in shape)} (got {tuple(t.shape)})")
+    if device is not None and t.get_device() != device:
+        _reject(f"{name} is on {t.device}, the call on cuda:{device}")
+    if shape is not None and (t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        _reject(f"{name} must have shape {tuple('any' if n is None else n for n in shape)} (got {tuple(t.shape)})")
     if contiguous and not t.is_contiguous():
         _reject(f"{name} must be contiguous")
 
@@ -430,21 +432,18 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return t.stride(0) if t.shape[0] > 1 else n
 
 
-class _on:
-    """The tensors' device as the current one while a call runs."""
+def _address(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, device):
-        self.index, self.prev = device.index, None
 
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.index:
-            self.prev = cur
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+def _launch(device: int, stream, fn, *args):
+    """The call on the tensors' device and its current stream (or the one given)."""
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == device:
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, handle))
 
 
 def sharq_kv_page_bytes(page_size: int, kv_heads: int, head_dim: int, fmt="nvfp4") -> int:
@@ -478,7 +477,7 @@ class KVCache:
         for name in ("k_scale", "v_scale"):
             t = getattr(self, name)
             if t is not None:
-                _tensor(t, name, torch.float32, self.pages.device)
+                _tensor(t, name, torch.float32, self.pages.get_device())
                 if t.numel() != self.kv_heads:
                     _reject(f"{name} must have one value per key head ({self.kv_heads}, got {t.numel()})")
         if _fmt(self.fmt) == SHARQ_MXFP4 and (self.k_scale is not None or self.v_scale is not None):
@@ -507,8 +506,8 @@ class KVBatch:
     def __post_init__(self):
         _tensor(self.kv_len, "kv_len", torch.int32, None, (None,))
         n = self.kv_len.numel()
-        _tensor(self.cu_q, "cu_q", torch.int32, self.kv_len.device, (n + 1,))
-        _tensor(self.page_table, "page_table", torch.int32, self.kv_len.device, (n, None))
+        _tensor(self.cu_q, "cu_q", torch.int32, self.kv_len.get_device(), (n + 1,))
+        _tensor(self.page_table, "page_table", torch.int32, self.kv_len.get_device(), (n, None))
         object.__setattr__(self, "c", _KVBatch(self.cu_q.data_ptr(), self.kv_len.data_ptr(), self.page_table.data_ptr(),
                                                n, self.page_table.shape[1], self.max_q, self.tokens))
 
@@ -522,10 +521,11 @@ def alloc_kv_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int,
                    k_scale, v_scale)
 
 
-def _same_device(cache: KVCache, batch: KVBatch):
-    if batch.kv_len.device != cache.pages.device:
+def _same_device(cache: KVCache, batch: KVBatch) -> int:
+    device = cache.pages.get_device()
+    if batch.kv_len.get_device() != device:
         _reject(f"the batch is on {batch.kv_len.device}, the cache on {cache.pages.device}")
-    return cache.pages.device
+    return device
 
 
 def sharq_kv_append(qkv: torch.Tensor, cache: KVCache, batch: KVBatch, q_heads: int,
@@ -546,14 +546,12 @@ def sharq_kv_append(qkv: torch.Tensor, cache: KVCache, batch: KVBatch, q_heads: 
     if inv_freq is not None:
         _tensor(inv_freq, "inv_freq", torch.float32, dev, (None,))
     if q_out is None:
-        q_out = torch.empty(batch.tokens, q_heads, d, dtype=torch.bfloat16, device=dev)
+        q_out = torch.empty(batch.tokens, q_heads, d, dtype=torch.bfloat16, device=cache.pages.device)
     else:
         _tensor(q_out, "q_out", torch.bfloat16, dev, (batch.tokens, q_heads, d))
-    with _on(dev):
-        _check(lib.sharq_kv_append(_ptr(qkv), stride, q_heads, ctypes.byref(cache.c), ctypes.byref(batch.c),
-                                   _ptr(q_gamma), _ptr(k_gamma), eps, _ptr(inv_freq),
-                                   0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), _ptr(q_out),
-                                   _stream(stream)))
+    _launch(dev, stream, lib.sharq_kv_append, qkv.data_ptr(), stride, q_heads, ctypes.byref(cache.c),
+            ctypes.byref(batch.c), _address(q_gamma), _address(k_gamma), eps, _address(inv_freq),
+            0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), q_out.data_ptr())
     return q_out
 
 
@@ -570,13 +568,12 @@ def sharq_kv_read(cache: KVCache, batch: KVBatch, k_out: torch.Tensor | None = N
         out_dtype = v_out.dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         _reject(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
-    k_out = torch.empty(shape, dtype=out_dtype, device=dev) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=out_dtype, device=dev) if v_out is None else v_out
+    k_out = torch.empty(shape, dtype=out_dtype, device=cache.pages.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=out_dtype, device=cache.pages.device) if v_out is None else v_out
     _tensor(k_out, "k_out", out_dtype, dev, shape)
     _tensor(v_out, "v_out", out_dtype, dev, shape)
-    with _on(dev):
-        _check(lib.sharq_kv_read(ctypes.byref(cache.c), ctypes.byref(batch.c), _ptr(k_out), _ptr(v_out),
-                                 SHARQ_OUT_F32 if out_dtype == torch.float32 else SHARQ_OUT_BF16, _stream(stream)))
+    _launch(dev, stream, lib.sharq_kv_read, ctypes.byref(cache.c), ctypes.byref(batch.c), k_out.data_ptr(),
+            v_out.data_ptr(), SHARQ_OUT_F32 if out_dtype == torch.float32 else SHARQ_OUT_BF16)
     return k_out, v_out
 
 
@@ -608,21 +605,20 @@ def sharq_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, causal: boo
     _tensor(q, "q", torch.bfloat16, dev, (batch.tokens, hq, d), contiguous=False)
     stride = _rows(q, "q")
     if y is None:
-        y = torch.empty(batch.tokens, hq, d, dtype=torch.bfloat16, device=dev)
+        y = torch.empty(batch.tokens, hq, d, dtype=torch.bfloat16, device=cache.pages.device)
     else:
         _tensor(y, "y", torch.bfloat16, dev, (batch.tokens, hq, d))
     if lse is not None:
         _tensor(lse, "lse", torch.float32, dev, (batch.tokens, hq))
     elif return_lse:
-        lse = torch.empty(batch.tokens, hq, dtype=torch.float32, device=dev)
+        lse = torch.empty(batch.tokens, hq, dtype=torch.float32, device=cache.pages.device)
     if workspace is None:
         workspace = alloc_attention_workspace(cache, batch, hq)
     else:
         _tensor(workspace, "workspace", torch.uint8, dev)
-    with _on(dev):
-        _check(lib.sharq_attention(_ptr(q), stride, hq, ctypes.byref(cache.c), ctypes.byref(batch.c), int(causal), window,
-                                   d ** -0.5 if scale is None else scale, _ptr(y), _ptr(lse), _ptr(workspace),
-                                   workspace.numel(), _stream(stream)))
+    _launch(dev, stream, lib.sharq_attention, q.data_ptr(), stride, hq, ctypes.byref(cache.c), ctypes.byref(batch.c),
+            int(causal), window, d ** -0.5 if scale is None else scale, y.data_ptr(), _address(lse),
+            workspace.data_ptr(), workspace.numel())
     return y if lse is None else (y, lse)
 
 
@@ -636,9 +632,10 @@ def sharq_norm_residual(y: torch.Tensor, residual: torch.Tensor, post_gamma: tor
     [gate_rows, k]; token t uses row t // rows_per_gate, or row 0 when rows_per_gate is 0) and the
     scaled residual stream. y, residual bf16 [tokens, k]. Returns (r', h); h is None without
     pre_gamma. residual_out may be residual, h_out may be y."""
-    _tensor(y, "y", torch.bfloat16, None, (None, None))
-    tokens, k = y.shape
-    dev = y.device
+    shape = y.shape if isinstance(y, torch.Tensor) and y.dim() == 2 else (None, None)
+    _tensor(y, "y", torch.bfloat16, y.get_device() if isinstance(y, torch.Tensor) and y.is_cuda else None, shape)
+    tokens, k = shape
+    dev = y.get_device()
     _tensor(residual, "residual", torch.bfloat16, dev, (tokens, k))
     for name, g in (("post_gamma", post_gamma), ("pre_gamma", pre_gamma)):
         if g is not None:
@@ -658,10 +655,9 @@ def sharq_norm_residual(y: torch.Tensor, residual: torch.Tensor, post_gamma: tor
         h_out = torch.empty_like(residual)
     else:
         _tensor(h_out, "h_out", torch.bfloat16, dev, (tokens, k))
-    with _on(dev):
-        _check(lib.sharq_norm_residual(_ptr(y), _ptr(residual), tokens, k, _ptr(post_gamma), _ptr(gate), gate_rows,
-                                       rows_per_gate, alpha, _ptr(pre_gamma), eps, _ptr(residual_out), _ptr(h_out),
-                                       _stream(stream)))
+    _launch(dev, stream, lib.sharq_norm_residual, y.data_ptr(), residual.data_ptr(), tokens, k, _address(post_gamma),
+            _address(gate), gate_rows, rows_per_gate, alpha, _address(pre_gamma), eps, residual_out.data_ptr(),
+            _address(h_out))
     return residual_out, h_out
 
 
