@@ -151,13 +151,12 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
       unpack8(cur, v);
       unpack8(cur_p, y);
       if (p.q_gamma || p.k_gamma) {  // block-uniform
-        float ss = 0.f;  // of values times 2^-8: the sum of D squares overflows no sooner than their mean
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i] * 0.00390625f, v[i], ss);
+        // in 64 bits: a rounding of the sum would move codes at the borders between two of them
+        double ss = add_squares_exact(cur.x, add_squares_exact(cur.y, add_squares_exact(cur.z, add_squares_exact(cur.w, 0.0))));
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float mean = ss * (256.f / D);
-        const float rstd = __frsqrt_rn(__fadd_rn(mean, p.eps));
+        const float mean = __double2float_rn(ss * (1.0 / D));
+        const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, p.eps)));
         if (gamma) {
           float g[8], gp[8];
           unpack8(gw, g);
