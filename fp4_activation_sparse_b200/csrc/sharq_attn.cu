@@ -36,16 +36,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// The warp waits for a stage's copies. After `limit_ns` the status word is set; the wait then goes
+// The warp waits for a stage's copies. A wait longer than `limit_ns` sets the status word and goes
 // on, bounded again, so that no copy is in flight when the block ends.
 __device__ __forceinline__ void wait_copies(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   uint64_t t0 = 0;
-  for (uint32_t i = 1; !kv_mbar_try(bar, parity); ++i) {
-    if (i & 31u) continue;
-    const uint64_t t = kv_globaltimer();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) atomicOr(&g_attn_rows_status, 1u);
-    if (t - t0 > limit_ns + kKvDrainLimitNs) break;
+  for (bool there = kv_mbar_test(bar, parity); !there;) {
+    const uint64_t waited = kv_waited_ns(&t0);
+    if (waited > limit_ns) atomicOr(&g_attn_rows_status, 1u);
+    if (waited > limit_ns + kKvDrainLimitNs) break;
+    there = kv_mbar_try(bar, parity);
+    if (there && kv_waited_ns(&t0) > limit_ns) atomicOr(&g_attn_rows_status, 1u);
   }
   __syncwarp();
 }

@@ -73,17 +73,18 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
 }
 // Gives up after `limit_ns`, or when another role of the block already did.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t *abort_flag) {
+  if (kv_mbar_test(bar, parity)) return true;
   uint64_t t0 = 0;
-  for (uint32_t i = 1; !kv_mbar_try(bar, parity); ++i) {
-    if (i & 31u) continue;
-    const uint64_t t = kv_globaltimer();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) {
+  kv_waited_ns(&t0);
+  bool there;
+  do {
+    there = kv_mbar_try(bar, parity);
+    if (kv_waited_ns(&t0) > limit_ns) {
       *abort_flag = 1u;
       atomicOr(&g_attn_status, 1u);
     }
     if (*abort_flag) return false;
-  }
+  } while (!there);
   return true;
 }
 // the same for a whole warp, which leaves the wait together
@@ -92,9 +93,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
   uint64_t t0 = 0;
   for (uint32_t i = 1; !__all_sync(0xFFFFFFFFu, kv_mbar_try(bar, parity)); ++i) {
     if (i & 31u) continue;
-    const uint64_t t = kv_globaltimer();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) {
+    if (kv_waited_ns(&t0) > limit_ns) {
       *abort_flag = 1u;
       atomicOr(&g_attn_status, 1u);
     }

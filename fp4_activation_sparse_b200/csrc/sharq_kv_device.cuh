@@ -34,10 +34,21 @@ __device__ __forceinline__ bool kv_mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ uint64_t kv_globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
+__device__ __forceinline__ bool kv_mbar_test(uint32_t bar, uint32_t parity) {  // without suspending the thread
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Time since `*t0` (set on the first call) in nanoseconds, at most: SM cycles of at least half a
+// nanosecond. (The global timer's steps of a microsecond hide a short wait.)
+__device__ __forceinline__ uint64_t kv_waited_ns(uint64_t *t0) {
+  const uint64_t t = (uint64_t)clock64();
+  if (*t0 == 0) *t0 = t;
+  return (t - *t0) >> 1;
 }
 __device__ __forceinline__ void kv_mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));

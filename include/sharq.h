@@ -374,6 +374,8 @@ int sharq_kv_read(const sharq_kv_cache *cache, const sharq_kv_batch *batch, void
  *                 ONCE before its first use; each call leaves it ready for the next, of any shape
  *                 that the buffer is large enough for. Calls whose launches may overlap on the GPU
  *                 (captured graphs that replay at once among them) need distinct workspaces.
+ * If a bounded device wait gives up, the call's outputs are undefined, sharq_device_status reports
+ * SHARQ_ERR_TIMEOUT, and the workspace must be zeroed again before it is reused.
  * A query that sees nothing gives y = 0 and lse = -inf. Scores, maxima, sums and outputs are
  * float32; probabilities enter the value product as float16 relative to a running maximum. */
 size_t sharq_attention_workspace_size(const sharq_kv_cache *cache, const sharq_kv_batch *batch, int q_heads);
