@@ -40,7 +40,7 @@ struct TokenPlace {
 
 // The places of `n` consecutive tokens. The block counts the sequences that end at or before the
 // first (one pass over cu_q, not a chain of dependent loads); a thread per token searches on.
-constexpr int kMaxTokens = 8;
+constexpr int kMaxTokens = 16;
 template <int D, bool MX>
 __device__ __forceinline__ void find_tokens(const KvBatchView &b, const KvCacheView &c, int token0, int n, TokenPlace *out) {
   constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
@@ -90,28 +90,31 @@ struct LanePlace {
   }
 };
 
-// Append: a block per one to eight tokens; D/8 lanes per head, eight elements per lane, a lane keeping
-// its head from token to token; partner elements and block maxima come by shuffles. cos and sin are formed once
-// per token from the 64-bit angle and rounded once. Bound by instructions near the rate of the
-// bytes (the row read once, q and the codes written once); several tokens per block share the
-// latency of finding their places and of the sines.
+// Append: a block per one to sixteen tokens; D/8 lanes per head, eight elements per lane, a lane
+// keeping its head from token to token; partner elements and block maxima come by shuffles. cos and
+// sin are formed once per token from the 64-bit angle and rounded once. Bound by its instructions
+// near the rate of the bytes (the row read once, q and the codes written once): 6417 rows of 40 heads
+// take 30 us bare, 33 us with the rotation and 41 us with both norms, against 19 us of bytes. Blocks fill
+// whole waves: five tokens a block in two waves and a bit took 47 us.
 template <int D, bool MX>
 __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p, int per_block) {
   constexpr int L = D / 8;  // lanes per head
   // cos and sin of angle f of a token at pair_place(f): the lanes of one load read neighbouring words
   constexpr int NC = D / 16;
   auto pair_place = [](int f) { return ((f & 7) >> 1) * (2 * NC) + (f >> 3) * 2 + (f & 1); };
-  __shared__ __align__(16) float2 turns[kMaxTokens][D / 2];
+  __shared__ __align__(16) float2 turns[kMaxTokens][2][D / 2];  // (cos, -sin) for the first of a pair, (cos, sin)
   __shared__ TokenPlace places[kMaxTokens];
   const int token0 = blockIdx.x * per_block, n = min(per_block, p.b.tokens - token0);
   const int kvh = p.c.kv_heads, heads = p.q_heads + 2 * kvh, at_once = blockDim.x / L;
   const int j = threadIdx.x % L, e0 = 8 * j;
   // the rows of two iterations ahead are on their way, the first while the places and sines are found
   int next_head = threadIdx.x / L, next_x = 0;
+  const uint16_t *next = p.qkv + (size_t)token0 * p.row_stride + (size_t)next_head * D + e0;
   auto fetch = [&]() {
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (next_head < heads) w = ld128(p.qkv + (size_t)(token0 + next_x) * p.row_stride + (size_t)next_head * D + e0);
-    if (++next_x == n) next_x = 0, next_head += at_once;
+    if (next_head < heads) w = ld128(next);
+    next += p.row_stride;
+    if (++next_x == n) next_x = 0, next_head += at_once, next += (long long)at_once * D - n * p.row_stride;
     return w;
   };
   uint4 ahead1 = fetch(), ahead2 = fetch();
@@ -120,7 +123,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
     const int x = i / p.rot_half, j = i - x * p.rot_half;
     double s, c;
     sincos((double)places[x].pos * (double)__ldg(p.inv_freq + j), &s, &c);
-    turns[x][pair_place(j)] = make_float2(__double2float_rn(c), __double2float_rn(s));
+    const float cf = __double2float_rn(c), sf = __double2float_rn(s);
+    turns[x][0][pair_place(j)] = make_float2(cf, -sf), turns[x][1][pair_place(j)] = make_float2(cf, sf);
   }
   __syncthreads();
   // whole warps stay in the loops: the shuffles below name every lane
@@ -134,23 +138,20 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
     const int partner = p.interleaved || !turned ? e0 : first ? e0 + p.rot_half : e0 - p.rot_half;
     const int f0 = p.interleaved ? e0 / 2 : first ? e0 : e0 - p.rot_half;
     const uint16_t *gamma = !live ? nullptr : is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr;
-    uint4 gw = make_uint4(0, 0, 0, 0), gwp = gw;
-    if (gamma) gw = ld128(gamma + e0), gwp = ld128(gamma + partner);
+    const bool norm = __any_sync(0xFFFFFFFFu, gamma != nullptr), swaps = __any_sync(0xFFFFFFFFu, partner != e0);
+    float g[8];
+    unpack8(gamma ? ld128(gamma + e0) : make_uint4(0, 0, 0, 0), g);
     const float *sp = is_k ? p.c.k_scale : p.c.v_scale;
     const float s = MX || !sp ? 1.f : __ldg(sp + kh), gain = __fdiv_rn(1.f, __fmul_rn(6.f, s));
     const int partner_lane = (threadIdx.x & 31) + (partner - e0) / 8;
-    const uint32_t flip = turned && !p.interleaved && first ? 0x80008000u : 0u;  // x1 c - x2 s
-    for (int x = 0; x < n; ++x) {
+    uint16_t *q_row = p.q_out + ((size_t)token0 * p.q_heads + head) * D + e0;
+    for (int x = 0; x < n; ++x, q_row += (size_t)p.q_heads * D) {
       const uint4 cur = ahead1;
       ahead1 = ahead2;
       ahead2 = fetch();
-      uint4 cur_p;
-      cur_p.x = __shfl_sync(0xFFFFFFFFu, cur.x, partner_lane) ^ flip, cur_p.y = __shfl_sync(0xFFFFFFFFu, cur.y, partner_lane) ^ flip;
-      cur_p.z = __shfl_sync(0xFFFFFFFFu, cur.z, partner_lane) ^ flip, cur_p.w = __shfl_sync(0xFFFFFFFFu, cur.w, partner_lane) ^ flip;
-      float v[8], y[8];
+      float v[8];
       unpack8(cur, v);
-      unpack8(cur_p, y);
-      if (p.q_gamma || p.k_gamma) {  // block-uniform
+      if (norm) {
         // in 64 bits: a rounding of the sum would move codes at the borders between two of them
         double ss = add_squares_exact(cur.x, add_squares_exact(cur.y, add_squares_exact(cur.z, add_squares_exact(cur.w, 0.0))));
 #pragma unroll
@@ -158,37 +159,34 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
         const float mean = __double2float_rn(ss * (1.0 / D));
         const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(mean, p.eps)));
         if (gamma) {
-          float g[8], gp[8];
-          unpack8(gw, g);
-          unpack8(gwp, gp);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] = __fmul_rn(__fmul_rn(v[i], rstd), g[i]);
-            y[i] = __fmul_rn(__fmul_rn(y[i], rstd), gp[i]);
-          }
+          for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rstd), g[i]);
         }
       }
-      if (turned) {
-        const float2 *turn = turns[x] + pair_place(f0);  // two angles are neighbours, the next two 2 NC on
-        if (p.interleaved) {
+      // two angles are neighbours, the next two 2 NC on
+      const float2 *turn = turns[x][p.interleaved || !first] + pair_place(f0);
+      if (swaps) {
+        float y[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 cs = turn[(i >> 1) * 2 * NC + (i & 1)];
-            const float a = v[2 * i], b = v[2 * i + 1];
-            v[2 * i] = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-            v[2 * i + 1] = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
-          }
-        } else {
+        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xFFFFFFFFu, v[i], partner_lane);
+        if (turned) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float2 cs = turn[(i >> 1) * 2 * NC + (i & 1)];
             v[i] = __fadd_rn(__fmul_rn(v[i], cs.x), __fmul_rn(y[i], cs.y));
           }
         }
+      } else if (turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 cs = turn[(i >> 1) * 2 * NC + (i & 1)];
+          const float a = v[2 * i], b = v[2 * i + 1];
+          v[2 * i] = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
+          v[2 * i + 1] = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+        }
       }
       const TokenPlace &tp = places[x];
-      if (is_q && tp.in_use)
-        *reinterpret_cast<uint4 *>(p.q_out + ((size_t)(token0 + x) * p.q_heads + head) * D + e0) = pack8_bf16(v);
+      if (is_q && tp.in_use) *reinterpret_cast<uint4 *>(q_row) = pack8_bf16(v);
       if (__all_sync(0xFFFFFFFFu, is_q || !live)) continue;
       // FP4 codes of the lane's eight elements; the block maximum spans two (four) lanes
       float am = 0.f;
@@ -217,8 +215,10 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(const AppendParams p,
   }
 }
 
-// Read: a block per one to eight tokens; a lane turns eight codes and their scale into values, the
-// same eight elements of four tokens at a time. code * block scale is exact in float16.
+// Read: a block per one to sixteen tokens; a lane turns eight codes and their scale into values, the
+// same eight elements of four tokens at a time. code * block scale is exact in float16. 32799 tokens
+// of eight key heads take 38 us, 4.5 TB/s; 72 us with a token per block, whose instructions to find
+// every unit's place were the bound.
 template <int D, bool MX>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams p, int per_block) {
   constexpr int L = D / 8, U = 4;
@@ -270,29 +270,30 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadParams p, int pe
   }
 }
 
-constexpr int kTokenBlocks = 8;  // per SM: 6417 rows of 40 heads 43 us, against 47 with 16 (read: 5.4 and 7.0)
-// Tokens per block: one while blocks are few (latency), up to eight once there are several waves.
-int tokens_per_block(int tokens) {
-  const int waves = tokens / (kTokenBlocks * sm_count());
-  return waves < 1 ? 1 : waves < kMaxTokens ? waves : kMaxTokens;
+// Tokens per block: one while every token finds a free slot on the SMs (latency), then as many as
+// fill whole waves of resident blocks (1024 threads of an SM: 64 registers each).
+int tokens_per_block(int tokens, int threads) {
+  const long long slots = (long long)sm_count() * (1024 / threads);
+  const long long waves = (tokens + slots * kMaxTokens - 1) / (slots * kMaxTokens);
+  return (int)((tokens + slots * waves - 1) / (slots * waves));
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t st) {
-  const int n = tokens_per_block(p.b.tokens), blocks = (p.b.tokens + n - 1) / n;
   const int lanes = (p.q_heads + 2 * p.c.kv_heads) * (d / 8);
   const int passes = (lanes + 255) / 256;
   const int threads = ((lanes + passes - 1) / passes + 31) / 32 * 32;  // whole warps, even passes
+  const int n = tokens_per_block(p.b.tokens, threads), blocks = (p.b.tokens + n - 1) / n;
   if (d == 128) (fmt ? kv_append_kernel<128, true> : kv_append_kernel<128, false>)<<<blocks, threads, 0, st>>>(p, n);
   else (fmt ? kv_append_kernel<64, true> : kv_append_kernel<64, false>)<<<blocks, threads, 0, st>>>(p, n);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const ReadParams &p, int d, int fmt, cudaStream_t st) {
-  const int n = tokens_per_block(p.b.tokens), blocks = (p.b.tokens + n - 1) / n;
   const int lanes = 2 * p.c.kv_heads * (d / 8);
   const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
+  const int n = tokens_per_block(p.b.tokens, threads), blocks = (p.b.tokens + n - 1) / n;
   if (d == 128) (fmt ? kv_read_kernel<128, true> : kv_read_kernel<128, false>)<<<blocks, threads, 0, st>>>(p, n);
   else (fmt ? kv_read_kernel<64, true> : kv_read_kernel<64, false>)<<<blocks, threads, 0, st>>>(p, n);
   return cudaGetLastError();
