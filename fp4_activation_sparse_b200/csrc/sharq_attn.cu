@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTile = 32;   // keys per step of a warp: two groups of the cache
-constexpr int kStagesA = 3;  // tiles in flight per warp
+constexpr int kStagesA = 2;  // tiles of a warp's ring: the next one loads while one is used (a third gained nothing)
 constexpr int kItemCost = 8;  // what an item costs besides its tiles (queries, joining eight warps), in tiles
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
