@@ -14,7 +14,12 @@
 // that ragged batches balance and a few long sequences fill the GPU; its eight warps walk a
 // segment's 32-key tiles in turn, each with copies of its own in flight, and join at its end. The
 // parts of an item that is cut between blocks go through the workspace; the block that arrives last
-// joins them in the order of the keys.
+// joins them in the order of the keys. Bulk copies (one per group of 16 tokens, issued by the lane that
+// looked up its page) keep the copying out of the instruction stream, which is the bound in
+// fact: about 640 instructions per 32 keys and warp, half of them turning codes into float16.
+//
+// Measured (32 query and 8 key heads of 128): 64 contexts of 33 to 8191 tokens 81 us, 3.8 TB/s; two of
+// 120 to 131 thousand 68 us, 4.0 TB/s; one of 777 tokens 10 us, which is latency.
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
 #include "sharq_kv.h"
@@ -550,7 +555,9 @@ cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
 }  // namespace
 
 namespace {
-// 32 rows: what one block of the kernel above can hold in registers
+// 32 rows: what one block of the kernel above holds in registers. At 20 rows (16 contexts of 1500 to
+// 6000 tokens, 4 key heads) it takes 39 us and the 128-row tiles 45, at 32 rows both 41; at 8 rows of
+// one context of 50000 tokens 33 and 96.
 bool use_tiles(const AttnParams &p) { return (long long)p.b.max_q * p.group > 32; }
 }  // namespace
 

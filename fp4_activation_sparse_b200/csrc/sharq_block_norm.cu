@@ -4,10 +4,11 @@
 //   h  = bf16(r' * rstd(r') * pre_gamma)   (optional; rstd of r' as stored)
 // Bound by its bytes: y and r read once, r' and h written once, 8 bytes per element. One block
 // per row keeps the row in registers between the two reductions, so nothing is read twice.
-// Measured: 32760 x 5120 with a gate and both norms 208 us, 6.46 TB/s (a plain copy's rate); 288 us while the
-// squares were added in float64 one by one and a second barrier handed the sum back (the loop was
-// then bound by its instructions); loading the next row ahead in a persistent block gained nothing.
-// Few rows take a unit per thread (16 x 4096: 3.0 us, against 5.1 with four).
+// Measured: 32760 x 5120 with a gate and both norms 208 us replayed on the same buffers (6.46 TB/s, a plain
+// copy's rate), 241 us on buffers that change; 288 us while the squares were added in float64 one by
+// one and a second barrier handed the sum back (the loop was then bound by its instructions).
+// Loading the next row ahead in a persistent block gained nothing. Few rows take a unit per thread
+// (16 x 4096: 3.0 us, against 5.1 with four).
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
 #include "sharq_kv.h"
