@@ -436,9 +436,17 @@ def _address(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _launch(device: int, stream, fn, *args):
-    """The call on the tensors' device and its current stream (or the one given)."""
-    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+def _on_stream(stream, device: torch.device):
+    """`stream` (a Stream or a raw handle) as the current one: what a call allocates and clears, and
+    what it launches, is then ordered on it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _launch(device: int, fn, *args):
+    """The call on the tensors' device and its current stream."""
+    handle = torch._C._cuda_getCurrentRawStream(device)
     if torch._C._cuda_getDevice() == device:
         _check(fn(*args, handle))
     else:
@@ -536,6 +544,9 @@ def sharq_kv_append(qkv: torch.Tensor, cache: KVCache, batch: KVBatch, q_heads: 
     QKV projection's output; rows may be strided): q and k are normalized per head where gammas
     are given, rotated by position * inv_freq (float32 [rot_dim/2]; None: no rotation), k and v
     quantized into the cache. Returns the queries, bf16 [tokens, q_heads, head_dim]."""
+    if stream is not None:
+        with _on_stream(stream, cache.pages.device):
+            return sharq_kv_append(qkv, cache, batch, q_heads, inv_freq, interleaved, q_gamma, k_gamma, eps, q_out)
     dev = _same_device(cache, batch)
     d, h = cache.head_dim, cache.kv_heads
     _tensor(qkv, "qkv", torch.bfloat16, dev, (batch.tokens, (q_heads + 2 * h) * d), contiguous=False)
@@ -549,7 +560,7 @@ def sharq_kv_append(qkv: torch.Tensor, cache: KVCache, batch: KVBatch, q_heads: 
         q_out = torch.empty(batch.tokens, q_heads, d, dtype=torch.bfloat16, device=cache.pages.device)
     else:
         _tensor(q_out, "q_out", torch.bfloat16, dev, (batch.tokens, q_heads, d))
-    _launch(dev, stream, lib.sharq_kv_append, qkv.data_ptr(), stride, q_heads, ctypes.byref(cache.c),
+    _launch(dev, lib.sharq_kv_append, qkv.data_ptr(), stride, q_heads, ctypes.byref(cache.c),
             ctypes.byref(batch.c), _address(q_gamma), _address(k_gamma), eps, _address(inv_freq),
             0 if inv_freq is None else 2 * inv_freq.numel(), int(interleaved), q_out.data_ptr())
     return q_out
@@ -560,6 +571,9 @@ def sharq_kv_read(cache: KVCache, batch: KVBatch, k_out: torch.Tensor | None = N
                   stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """The batch's token rows of the cache as values: (k, v), [tokens, kv_heads, head_dim], bf16
     or float32."""
+    if stream is not None:
+        with _on_stream(stream, cache.pages.device):
+            return sharq_kv_read(cache, batch, k_out, v_out, out_dtype)
     dev = _same_device(cache, batch)
     shape = (batch.tokens, cache.kv_heads, cache.head_dim)
     if k_out is not None:
@@ -572,7 +586,7 @@ def sharq_kv_read(cache: KVCache, batch: KVBatch, k_out: torch.Tensor | None = N
     v_out = torch.empty(shape, dtype=out_dtype, device=cache.pages.device) if v_out is None else v_out
     _tensor(k_out, "k_out", out_dtype, dev, shape)
     _tensor(v_out, "v_out", out_dtype, dev, shape)
-    _launch(dev, stream, lib.sharq_kv_read, ctypes.byref(cache.c), ctypes.byref(batch.c), k_out.data_ptr(),
+    _launch(dev, lib.sharq_kv_read, ctypes.byref(cache.c), ctypes.byref(batch.c), k_out.data_ptr(),
             v_out.data_ptr(), SHARQ_OUT_F32 if out_dtype == torch.float32 else SHARQ_OUT_BF16)
     return k_out, v_out
 
@@ -599,6 +613,9 @@ def sharq_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, causal: boo
     [tokens, q_heads], the natural log of the sum of exponentials). `window` > 0 (causal only):
     the last `window` positions. scale defaults to head_dim ** -0.5. `workspace` as from
     alloc_attention_workspace (allocated here if omitted)."""
+    if stream is not None:
+        with _on_stream(stream, cache.pages.device):
+            return sharq_attention(q, cache, batch, causal, window, scale, return_lse, y, lse, workspace)
     dev = _same_device(cache, batch)
     d = cache.head_dim
     hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else 0
@@ -616,7 +633,7 @@ def sharq_attention(q: torch.Tensor, cache: KVCache, batch: KVBatch, causal: boo
         workspace = alloc_attention_workspace(cache, batch, hq)
     else:
         _tensor(workspace, "workspace", torch.uint8, dev)
-    _launch(dev, stream, lib.sharq_attention, q.data_ptr(), stride, hq, ctypes.byref(cache.c), ctypes.byref(batch.c),
+    _launch(dev, lib.sharq_attention, q.data_ptr(), stride, hq, ctypes.byref(cache.c), ctypes.byref(batch.c),
             int(causal), window, d ** -0.5 if scale is None else scale, y.data_ptr(), _address(lse),
             workspace.data_ptr(), workspace.numel())
     return y if lse is None else (y, lse)
@@ -632,6 +649,10 @@ def sharq_norm_residual(y: torch.Tensor, residual: torch.Tensor, post_gamma: tor
     [gate_rows, k]; token t uses row t // rows_per_gate, or row 0 when rows_per_gate is 0) and the
     scaled residual stream. y, residual bf16 [tokens, k]. Returns (r', h); h is None without
     pre_gamma. residual_out may be residual, h_out may be y."""
+    if stream is not None and isinstance(y, torch.Tensor):
+        with _on_stream(stream, y.device):
+            return sharq_norm_residual(y, residual, post_gamma, gate, rows_per_gate, alpha, pre_gamma, eps, residual_out,
+                                       h_out)
     shape = y.shape if isinstance(y, torch.Tensor) and y.dim() == 2 else (None, None)
     _tensor(y, "y", torch.bfloat16, y.get_device() if isinstance(y, torch.Tensor) and y.is_cuda else None, shape)
     tokens, k = shape
@@ -655,7 +676,7 @@ def sharq_norm_residual(y: torch.Tensor, residual: torch.Tensor, post_gamma: tor
         h_out = torch.empty_like(residual)
     else:
         _tensor(h_out, "h_out", torch.bfloat16, dev, (tokens, k))
-    _launch(dev, stream, lib.sharq_norm_residual, y.data_ptr(), residual.data_ptr(), tokens, k, _address(post_gamma),
+    _launch(dev, lib.sharq_norm_residual, y.data_ptr(), residual.data_ptr(), tokens, k, _address(post_gamma),
             _address(gate), gate_rows, rows_per_gate, alpha, _address(pre_gamma), eps, residual_out.data_ptr(),
             _address(h_out))
     return residual_out, h_out

@@ -527,6 +527,7 @@ int sharq_kv_append(const void *qkv, long long row_stride, int q_heads, const sh
     return SHARQ_OK;
   }
   if (!qkv || !q_out) return fail(SHARQ_ERR_INVALID_ARG, "null qkv or output");
+  if (qkv == q_out) return fail(SHARQ_ERR_INVALID_ARG, "q_out must be another buffer than qkv");
   if (!aligned16(qkv) || !aligned16(q_out)) return fail(SHARQ_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
   p.qkv = static_cast<const uint16_t *>(qkv);
   p.row_stride = row_stride;
@@ -601,6 +602,7 @@ int sharq_attention(const void *q, long long q_stride, int q_heads, const sharq_
     return SHARQ_OK;
   }
   if (!q || !y) return fail(SHARQ_ERR_INVALID_ARG, "null q or output");
+  if (q == y) return fail(SHARQ_ERR_INVALID_ARG, "y must be another buffer than q");
   if (!aligned16(q) || !aligned16(y)) return fail(SHARQ_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
   const size_t need = sharq::attention_workspace(p, d);
   if (!workspace || workspace_bytes < need)
@@ -640,6 +642,7 @@ int sharq_norm_residual(const void *y, const void *residual, int tokens, int k, 
   }
   if (!y || !residual || !residual_out || (pre_gamma && !h_out))
     return fail(SHARQ_ERR_INVALID_ARG, "null y, residual or output");
+  if (pre_gamma && h_out == residual_out) return fail(SHARQ_ERR_INVALID_ARG, "h_out and residual_out must be two buffers");
   if (!aligned16(y) || !aligned16(residual) || !aligned16(residual_out) || !aligned16(h_out) || !aligned16(gate) ||
       !aligned16(post_gamma) || !aligned16(pre_gamma))
     return fail(SHARQ_ERR_INVALID_ARG, "buffers must be 16-byte aligned");

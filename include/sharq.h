@@ -368,7 +368,7 @@ int sharq_kv_read(const sharq_kv_cache *cache, const sharq_kv_batch *batch, void
  *                 appended), and with window > 0 only the last `window` of them; otherwise every
  *                 position below kv_len (window must be 0)
  *   scale         factor of q . k (commonly 1/sqrt(head_dim)), finite
- *   y_dev         [tokens][q_heads][head_dim] bf16
+ *   y_dev         [tokens][q_heads][head_dim] bf16; may not overlap q
  *   lse_dev       [tokens][q_heads] float32 natural log of the sum of exponentials, or NULL
  *   workspace_dev device buffer of sharq_attention_workspace_size bytes, 16-byte aligned, ZEROED
  *                 ONCE before its first use; each call leaves it ready for the next, of any shape

@@ -187,6 +187,58 @@ def test_many_sequences_of_uneven_length():
     run(S, st, new, 2)
 
 
+def test_more_entries_than_threads():
+    """Many sequences of several row tiles each, uneven and some empty."""
+    S = require_gpu()
+    rng = np.random.default_rng(13)
+    lengths = rng.integers(0, 140, 260).tolist()
+    lengths[3], lengths[200] = 700, 1500
+    new = [int(min(n, rng.integers(0, 140))) for n in lengths]
+    st = Setup(S, rng, lengths, 1, 64, "nvfp4", 16).fill()
+    run(S, st, new, 4)
+
+
+@pytest.mark.parametrize("group,new", [(40, 1), (128, 1), (128, 3), (33, 8)])
+def test_large_groups(group, new):
+    S = require_gpu()
+    st = Setup(S, np.random.default_rng(group), [200, 5, 900], 1, 64, "mxfp4", 32).fill()
+    run(S, st, [new, min(new, 5), new], group)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_nothing_but_padding_and_nothing_cached(new):
+    S = require_gpu()
+    rng = np.random.default_rng(6)
+    st = Setup(S, rng, [50, 40], 2, 128, "nvfp4", 16).fill()
+    q, x = bf16(rng, new, 4, 128)
+    y = torch.full((new, 4, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((new, 4), 9.0, device="cuda")
+    S.sharq_attention(q, st.cache, st.batch([0, 0], tokens=new, max_q=new), y=y, lse=lse)
+    assert (y == 3).all() and (lse == 9).all()
+    S.sharq_attention(q, st.cache, st.batch([new, 0], [0, 0]), causal=False, y=y, lse=lse)
+    assert not y.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_on_a_stream_of_its_own(new):
+    """A call given a stream orders its workspace and outputs there, behind that stream's work."""
+    S = require_gpu()
+    rng = np.random.default_rng(17)
+    st = Setup(S, rng, [1200, 900], 2, 128, "nvfp4", 16).fill()
+    q, x = bf16(rng, 2 * new, 8, 128)
+    batch = st.batch([new, new])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    late = torch.zeros_like(q)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about ten milliseconds
+        late.copy_(q)
+    for handle in (side, side.cuda_stream):
+        y, lse = S.sharq_attention(late, st.cache, batch, return_lse=True, stream=handle)
+        side.synchronize()
+        check_rows(S, st, x, y, lse, [new, new], st.lengths)
+
+
 @pytest.mark.parametrize("new", [1, 4, 300])
 def test_same_inputs_same_bits(new):
     S = require_gpu()
@@ -280,7 +332,7 @@ def test_refusals():
     for bad in (q.float(), q[:1], q[..., :32], q[:, :3], q.transpose(0, 1).contiguous().transpose(0, 1), q.cpu()):
         with pytest.raises(S.SharqError):
             S.sharq_attention(bad, st.cache, batch)
-    for kw in (dict(causal=False, window=3), dict(window=-1), dict(scale=float("nan")), dict(y=q[:1]), dict(lse=q),
+    for kw in (dict(causal=False, window=3), dict(window=-1), dict(scale=float("nan")), dict(y=q[:1]), dict(y=q), dict(lse=q),
                dict(workspace=torch.zeros(1, dtype=torch.uint8, device="cuda")[:0])):
         with pytest.raises(S.SharqError):
             S.sharq_attention(q, st.cache, batch, **kw)

@@ -100,7 +100,7 @@ def test_refusals():
     z = torch.zeros(6, 64, dtype=torch.bfloat16, device="cuda")
     for kw in (dict(residual=z[:5]), dict(residual=z.float()), dict(post_gamma=z[0, :32]), dict(gate=z[:2], rows_per_gate=2),
                dict(gate=z, rows_per_gate=-1), dict(h_out=z), dict(alpha=float("nan")), dict(eps=-1.0, pre_gamma=z[0]),
-               dict(residual_out=z[:, :32])):
+               dict(residual_out=z[:, :32]), dict(residual_out=z, h_out=z, pre_gamma=z[0])):
         with pytest.raises(S.SharqError):
             S.sharq_norm_residual(z, **{"residual": z, **kw})
     with pytest.raises(S.SharqError):
