@@ -624,6 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       const bool real = live && token >= 0 && token < p.b.tokens;
       const float v_scale = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + w.kh);
       uint16_t *dst = p.y + ((size_t)token * p.q_heads + head) * D;
+      const bool wide = ((uintptr_t)p.y & 31u) == 0;  // whole 32-byte sectors at once
       auto put = [&](int x, const float *o, float f) {  // 32 elements of the row
         uint32_t out[16];
 #pragma unroll
@@ -631,7 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
           const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * j] * f, o[2 * j + 1] * f);
           out[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        if (real) st256(dst + 32 * x, out), st256(dst + 32 * x + 16, out + 8);
+        if (!real) return;
+        if (wide) {
+          st256(dst + 32 * x, out), st256(dst + 32 * x + 16, out + 8);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<uint4 *>(dst + 32 * x)[j] = make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+        }
       };
       auto put_lse = [&](float mm, float ll) {
         if (real && p.lse)
@@ -862,6 +870,7 @@ int row_tiles(const AttnParams &p) {
 template <int D, bool MX>
 cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
   auto kernel = attn_tiles_kernel<D, MX>;
+  if ((long long)p.b.n_seq * row_tiles(p) > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   static SmemOnce once;
   if (cudaError_t e = once.set(kernel, TileSmem<D>::kTotal)) return e;
   kernel<<<sm_count(), kThreads, TileSmem<D>::kTotal, st>>>(p, row_tiles(p));

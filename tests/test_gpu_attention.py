@@ -187,6 +187,36 @@ def test_many_sequences_of_uneven_length():
     run(S, st, new, 2)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 70])
+def test_buffers_at_their_least_alignment(new, d):
+    """Every buffer 16 bytes (lse and indexes 4) off a round address."""
+    S = require_gpu()
+    rng = np.random.default_rng(19)
+    st = Setup(S, rng, [200, 150], 2, d, "nvfp4", 16).fill()
+
+    def off(t, by):
+        n = by // t.element_size()
+        out = torch.zeros(t.numel() + 2 * n, dtype=t.dtype, device="cuda")[n:n + t.numel()].view(t.shape)
+        out.copy_(t)
+        assert out.data_ptr() % (2 * by) == by
+        return out
+
+    cache = S.KVCache(off(st.cache.pages, 16), st.num_pages, 16, 2, d, "nvfp4", off(st.cache.k_scale, 4), off(st.cache.v_scale, 4))
+    q, x = bf16(rng, 2 * new, 8, d)
+    q = off(q, 16)
+    y, lse = off(torch.zeros_like(q), 16), off(torch.zeros(2 * new, 8, device="cuda"), 4)
+    b = st.batch([new, new])
+    batch = S.KVBatch(off(b.cu_q, 4), off(b.kv_len, 4), off(b.page_table, 4), new, 2 * new)
+    ws = S.alloc_attention_workspace(cache, batch, 8)
+    S.sharq_attention(q, cache, batch, y=y, lse=lse, workspace=off(ws, 16))
+    check_rows(S, st, x, y, lse, [new, new], st.lengths)
+    k, v = S.sharq_kv_read(cache, batch, off(torch.zeros(2 * new, 2, d, device="cuda"), 16),
+                           off(torch.zeros(2 * new, 2, d, device="cuda"), 16))
+    k2, v2 = S.sharq_kv_read(st.cache, b, out_dtype=torch.float32)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+
+
 def test_more_entries_than_threads():
     """Many sequences of several row tiles each, uneven and some empty."""
     S = require_gpu()
