@@ -84,7 +84,7 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-// Gives up after `limit_ns`, or when another role of the block already did.
+// One thread. Gives up after `limit_ns`, or when another role of the block already did.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t *abort_flag) {
   if (kv_mbar_test(bar, parity)) return true;
   uint64_t t0 = 0;
@@ -453,7 +453,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
   __shared__ long long warp_sums[kThreads / 32];
   __shared__ float row_coef[2 * kRows];  // score factor of each row of the segment
   __shared__ uint32_t tmem_slot;
-  __shared__ uint32_t last_part[2];
   __shared__ volatile uint32_t abort_flag;
   __shared__ volatile uint32_t valid[kValidRing];  // a byte per dequantizing warp: two groups' bits
 
@@ -679,16 +678,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         continue;
       }
       if (live) __stcg(mine + D * kRows, m), __stcg(mine + (D + 1) * kRows, l);
+      // Each warp joins its own 32 rows with the same warp of the item's other parts: a barrier among the
+      // four would wait without limit for a warp that gave up.
       __threadfence();
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
-      if (r == 0) {
-        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + 2 * w.parts.owner + t;
-        const uint32_t before = atomicAdd(counter, 1u);
-        last_part[t] = before + 1 == (uint32_t)w.parts.count;
-        if (last_part[t]) *counter = 0;  // ready for the next call
+      __syncwarp();
+      uint32_t arrived_last = 0;
+      if (lane == 0) {
+        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + 8 * w.parts.owner + warp;
+        arrived_last = atomicAdd(counter, 1u) + 1 == (uint32_t)w.parts.count;
+        if (arrived_last) *counter = 0;  // ready for the next call
       }
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
-      if (!last_part[t]) continue;
+      if (!__shfl_sync(0xFFFFFFFFu, arrived_last, 0)) continue;
       __threadfence();
       if (!live) continue;
       float mm = -INFINITY, ll = 0.f;
@@ -719,6 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
     const int dw = warp - 8, group_mask = (1 << (p.c.page_shift - 4)) - 1;
     int n = 0;  // key steps of all segments
     bool ok = true;
+    // the lanes go on or give up together: those left behind would wait for the others without limit
+    auto wait = [&](const uint64_t &b, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar(b), parity, limit, &abort_flag));
+    };
     for (int seg = 0; ok && get_work(bars, ring, seg, limit, &abort_flag); ++seg) {
       const int begin = ring[seg & 1].r.begin, end = ring[seg & 1].r.end, kv_len = ring[seg & 1].r.kv_len, kh = ring[seg & 1].kh;
       const int *table = p.b.page_table + (size_t)ring[seg & 1].seq * p.b.max_pages;
@@ -745,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         if (i + 1 < end) {
           const int nk = n + 1 + i - begin, st = nk & 1;
           const uint32_t bits = (k_grp[0] ? 1u : 0u) | (k_grp[1] ? 2u : 0u);
-          if (nk >= 2 && !(ok = mbar_wait(bar(bars.k_empty[st]), ((nk >> 1) - 1) & 1, limit, &abort_flag))) break;
+          if (nk >= 2 && !(ok = wait(bars.k_empty[st], ((nk >> 1) - 1) & 1))) break;
           store_k<D, MX>(base + M::kK + st * M::kTile, 32 * dw, lane, ck);
           if (lane == 0) reinterpret_cast<volatile uint8_t *>(&valid[nk % kValidRing])[dw] = (uint8_t)bits;
           fence_proxy_async();
@@ -757,14 +761,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         load_k<D, MX>(k_grp, lane, ck);
         if (i < begin) continue;
         const int nv = n + i - begin, st = nv & 1;
-        if (nv >= 2 && !(ok = mbar_wait(bar(bars.v_empty[st]), ((nv >> 1) - 1) & 1, limit, &abort_flag))) break;
+        if (nv >= 2 && !(ok = wait(bars.v_empty[st], ((nv >> 1) - 1) & 1))) break;
         store_v<D, MX>(base + M::kV + st * M::kTile, 32 * dw, lane, kv_len - (i * kKeys + 32 * dw), cv);
         fence_proxy_async();
         mbar_arrive_warp(bar(bars.v_full[st]));
         load_v<D, MX>(v_grp, lane, cv);
       }
       n += end - begin;
-      ok = __all_sync(0xFFFFFFFFu, ok);
     }
   } else if (warp < 14) {
     // ------------------------------------------------------------------ MMA issue
