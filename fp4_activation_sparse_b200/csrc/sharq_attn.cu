@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       if (at < first + (long long)cost * p.c.kv_heads) break;
       first += (long long)cost * p.c.kv_heads;
     }
-    const int kh = (int)((at - first) / cost);
+    const int kh = small_quotient(at - first, cost);
     const long long p0 = first + (long long)kh * cost, p1 = p0 + cost, to = min(share.cut[1], p1);
     const ItemParts parts = item_parts<kItemCost>(share, p0, p1, at);
     int t_lo = w.lo, t_hi = w.hi;
@@ -509,15 +509,30 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
         __threadfence();
         for (int idx = threadIdx.x; idx < rows * F4; idx += kWarps * 32) {
           const int row = idx / F4, i4 = idx % F4;
+          // eight parts' loads are in flight at once; references move from eight to eight
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           float mm = -INFINITY, ll = 0.f;
-          for (int j = 0; j < parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + C::R * D + 2 * row));
-          for (int j = 0; j < parts.count; ++j) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_at(j) + C::R * D) + row);
-            const float f = kv_ex2(ml.x - (mm == -INFINITY ? 0.f : mm));
-            const float4 u = __ldcg(reinterpret_cast<const float4 *>(part_at(j)) + idx);
-            ll += ml.y * f;
-            v.x = fmaf(u.x, f, v.x), v.y = fmaf(u.y, f, v.y), v.z = fmaf(u.z, f, v.z), v.w = fmaf(u.w, f, v.w);
+          for (int j0 = 0; j0 < parts.count; j0 += 8) {
+            float2 ml[8];
+            float4 u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const bool some = j0 + j < parts.count;
+              ml[j] = some ? __ldcg(reinterpret_cast<const float2 *>(part_at(j0 + j) + C::R * D) + row) : make_float2(-INFINITY, 0.f);
+              u[j] = some ? __ldcg(reinterpret_cast<const float4 *>(part_at(j0 + j)) + idx) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float top = mm;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, ml[j].x);
+            const float ref = top == -INFINITY ? 0.f : top, keep = kv_ex2(mm - ref);
+            mm = top;
+            ll *= keep, v.x *= keep, v.y *= keep, v.z *= keep, v.w *= keep;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float f = kv_ex2(ml[j].x - ref);
+              ll += ml[j].y * f;
+              v.x = fmaf(u[j].x, f, v.x), v.y = fmaf(u[j].y, f, v.y), v.z = fmaf(u[j].z, f, v.z), v.w = fmaf(u[j].w, f, v.w);
+            }
           }
           put(row, i4, v, mm, ll);
         }

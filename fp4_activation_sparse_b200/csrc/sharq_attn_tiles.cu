@@ -381,7 +381,7 @@ __device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles,
     first += (long long)cost * heads;
   }
   sh.first = first;
-  x.kh = (int)((at - first) / cost);
+  x.kh = small_quotient(at - first, cost);
   const long long p0 = first + (long long)x.kh * cost, p1 = p0 + cost;
   const long long to = min(sh.cut[1], p1);
   x.parts = item_parts<kItemCost>(sh, p0, p1, at);
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   find_share<kThreads, kItemCost>((long long)p.b.n_seq * row_tiles, p.c.kv_heads, kItemCost + 2, &share, warp_sums,
-                                  [&](long long e) { return item_range(p, (int)(e / row_tiles), (int)(e % row_tiles)).cost(); });
+                                  [&](long long e) { return item_range(p, (int)e / row_tiles, (int)e % row_tiles).cost(); });
   if (share.cut[0] >= share.cut[1]) return;
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem_u32(&tmem_slot)), "r"(kTmemCols));
@@ -645,11 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
           p.lse[(size_t)token * p.q_heads + head] = ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * 0.69314718055994531f;
       };
       const float inv = l == 0.f ? 0.f : v_scale / l;
-      // parts: [block][first or not][row tile]: O by column, then m and l
+      // parts: [block][first or not][row tile]: O as [4 elements][row], then m and l by row
       const int tiles = p.b.max_q * p.group > kRows ? 2 : 1;
       float *const parts = reinterpret_cast<float *>(p.workspace + kAttnCounterBytes);
       auto part_at = [&](int j) {
-        return parts + (((size_t)(w.parts.owner + j) * 2 + (j == 0 ? 1 : 0)) * tiles + t) * kRows * (D + 2) + r;
+        return parts + (((size_t)(w.parts.owner + j) * 2 + (j == 0 ? 1 : 0)) * tiles + t) * kRows * (D + 2);
       };
       float *mine = part_at(w.parts.index);
 #pragma unroll 1
@@ -666,7 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         if (w.parts.count == 1) put(x, o, inv);
         else if (live) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) __stcg(mine + (32 * x + j) * kRows, o[j]);
+          for (int j = 0; j < 8; ++j)
+            __stcg(reinterpret_cast<float4 *>(mine) + (8 * x + j) * kRows + r,
+                   make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
         }
       }
       if (any) {
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         put_lse(m, l);
         continue;
       }
-      if (live) __stcg(mine + D * kRows, m), __stcg(mine + (D + 1) * kRows, l);
+      if (live) __stcg(reinterpret_cast<float2 *>(mine + D * kRows) + r, make_float2(m, l));
       // Each warp joins its own 32 rows with the same warp of the item's other parts: a barrier among the
       // four would wait without limit for a warp that gave up.
       __threadfence();
@@ -691,22 +693,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       if (!__shfl_sync(0xFFFFFFFFu, arrived_last, 0)) continue;
       __threadfence();
       if (!live) continue;
-      float mm = -INFINITY, ll = 0.f;
-      for (int j = 0; j < w.parts.count; ++j) mm = fmaxf(mm, __ldcg(part_at(j) + D * kRows));
+      // Latency is most of the joining: the first four parts' (more are rare) m and l are loaded at once,
+      // O by two parts. (Four parts of O at once took registers that the prompt's loop missed: 1 % there,
+      // for 1 % of the drafted tokens.)
+      auto ml_at = [&](int j) { return __ldcg(reinterpret_cast<const float2 *>(part_at(j) + D * kRows) + r); };
+      float2 ml[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ml[j] = j < w.parts.count ? ml_at(j) : make_float2(-INFINITY, 0.f);
+      float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), ll = 0.f, f[4];
+      for (int j = 4; j < w.parts.count; ++j) mm = fmaxf(mm, ml_at(j).x);
       const float ref = mm == -INFINITY ? 0.f : mm;
-      for (int j = 0; j < w.parts.count; ++j)
-        ll += __ldcg(part_at(j) + (D + 1) * kRows) * kv_ex2(__ldcg(part_at(j) + D * kRows) - ref);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = kv_ex2(ml[j].x - ref), ll += ml[j].y * f[j];
+      for (int j = 4; j < w.parts.count; ++j) {
+        const float2 v = ml_at(j);
+        ll += v.y * kv_ex2(v.x - ref);
+      }
       const float inv_all = ll == 0.f ? 0.f : v_scale / ll;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
+        auto o_at = [&](int j, int e) { return __ldcg(reinterpret_cast<const float4 *>(part_at(j)) + (8 * x + e) * kRows + r); };
         float o[32];
+        auto add = [&](const float4 (&v)[8], float g) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            o[4 * e] = fmaf(v[e].x, g, o[4 * e]), o[4 * e + 1] = fmaf(v[e].y, g, o[4 * e + 1]);
+            o[4 * e + 2] = fmaf(v[e].z, g, o[4 * e + 2]), o[4 * e + 3] = fmaf(v[e].w, g, o[4 * e + 3]);
+          }
+        };
+        float4 v[2][8];
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = 0.f;
-        for (int j = 0; j < w.parts.count; ++j) {
-          const float *src = part_at(j);
-          const float f = kv_ex2(__ldcg(src + D * kRows) - ref);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = fmaf(__ldcg(src + (32 * x + e) * kRows), f, o[e]);
+        for (int j0 = 0; j0 < 4; j0 += 2) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = j0 + j < w.parts.count ? o_at(j0 + j, e) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) add(v[j], f[j0 + j]);
+        }
+        for (int j = 4; j < w.parts.count; ++j) {
+          const float g = kv_ex2(ml_at(j).x - ref);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[0][e] = o_at(j, e);
+          add(v[0], g);
         }
         put(x, o, inv_all);
       }

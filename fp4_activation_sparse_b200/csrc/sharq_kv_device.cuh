@@ -95,6 +95,8 @@ struct Share {
   long long total, blocks;  // cost of the launch, blocks that have a share
   long long cut[2];         // begin and end of the share
   long long first;          // where the entry that the share begins in begins
+  long long per;            // total = per * blocks + rest
+  int rest;
   int entry, snap;
 };
 // An item's parts: how many, which one a block has, and the block of the first.
@@ -102,8 +104,19 @@ struct ItemParts {
   int count, index, owner;
 };
 
+// a / b for a quotient below 2^20: float32 finds it to within one. (A 64-bit division takes a few hundred
+// cycles; a block makes several in a row before its first load.)
+__device__ __forceinline__ int small_quotient(long long a, long long b) {
+  int q = (int)__fdividef((float)a, (float)b);
+  const long long r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
+}
+
+// block * total / blocks
 __device__ __forceinline__ long long raw_cut(const Share &s, long long block) {
-  return block >= s.blocks ? s.total : block * s.total / s.blocks;
+  return block >= s.blocks ? s.total : block * s.per + (uint32_t)block * (uint32_t)s.rest / (uint32_t)s.blocks;
 }
 
 // All threads: the entries' costs are summed in chunks of the block size, then the entries that
@@ -136,11 +149,11 @@ __device__ __forceinline__ void find_share(long long entries, int heads, int lea
         }
       }
       if (pass == 1 && cost > 0) {
-        const int item = (int)(cost / heads);
+        const int item = (int)((uint64_t)cost >> 32 ? cost / heads : (uint32_t)cost / (uint32_t)heads);
         for (int i = 0; i < 2; ++i) {
           const long long x = raw_cut(*sh, (long long)blockIdx.x + i);
           if (x < before || x >= before + cost) continue;
-          const long long p0 = before + (x - before) / item * item;
+          const long long p0 = before + (long long)small_quotient(x - before, item) * item;
           sh->cut[i] = x - p0 <= ITEM + sh->snap ? p0 : p0 + item - x <= sh->snap ? p0 + item : x;
           if (i == 0) sh->entry = (int)e, sh->first = before;
         }
@@ -150,8 +163,10 @@ __device__ __forceinline__ void find_share(long long entries, int heads, int lea
       total = base;
       if (threadIdx.x == 0) {
         sh->total = total;
-        sh->blocks = min((long long)gridDim.x, max(1ll, total / least));
-        sh->snap = (int)min(2ll, total / sh->blocks / 4);
+        const uint32_t blocks = total >= (long long)gridDim.x * least ? gridDim.x : max(1u, (uint32_t)total / (uint32_t)least);
+        const long long per = (uint64_t)total >> 32 ? total / blocks : (uint32_t)total / blocks;
+        sh->blocks = blocks, sh->per = per, sh->rest = (int)(total - per * blocks);
+        sh->snap = total >= 8ll * blocks ? 2 : total >= 4ll * blocks ? 1 : 0;
         sh->cut[0] = sh->cut[1] = total;  // ends that no entry holds
         sh->entry = 0, sh->first = 0;
       }
@@ -165,9 +180,9 @@ __device__ __forceinline__ void find_share(long long entries, int heads, int lea
 // inside it are those with p0 + ITEM + snap < raw_cut(block) < p1 - snap.
 template <int ITEM>
 __device__ __forceinline__ ItemParts item_parts(const Share &s, long long p0, long long p1, long long from) {
-  const long long lo = ((p0 + ITEM + s.snap + 1) * s.blocks + s.total - 1) / s.total;
-  const long long hi = min(((p1 - s.snap) * s.blocks + s.total - 1) / s.total - 1, s.blocks - 1);
-  return ItemParts{hi >= lo ? (int)(hi - lo + 2) : 1, from == p0 ? 0 : (int)(blockIdx.x - lo + 1), (int)lo - 1};
+  const int lo = small_quotient((p0 + ITEM + s.snap + 1) * s.blocks + s.total - 1, s.total);
+  const int hi = min(small_quotient((p1 - s.snap) * s.blocks + s.total - 1, s.total) - 1, (int)s.blocks - 1);
+  return ItemParts{hi >= lo ? hi - lo + 2 : 1, from == p0 ? 0 : (int)blockIdx.x - lo + 1, lo - 1};
 }
 
 }  // namespace sharq
