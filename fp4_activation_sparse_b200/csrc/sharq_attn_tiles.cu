@@ -29,6 +29,11 @@
 // one is in its softmax. A query block whose steps are cut between blocks leaves its parts (O, m, l
 // in float32) in the workspace; the block that arrives last joins them in the order of the keys.
 //
+// Where a key head has no more than 128 rows (drafted tokens, short prompts) the two tiles are twins: both
+// hold the same rows and take every second key step, so that two softmax chains run at once instead of
+// one. The first tile's warps join the two outputs as they read them from tensor memory. (Drafted
+// tokens, 35 rows: 41.0 us with one tile idle, 39.4 with twins.)
+//
 // What bounds it. A step (256 rows, 128 keys, 128 elements) takes about 4200 cycles per SM. Its products
 // need 2480 on the tensor pipe (the score halves, N = 64, are bound by reading Q and K from shared
 // memory: 1540, against 1020 in one piece; the halves pay for that by hiding the latency between
@@ -73,6 +78,7 @@ struct TileSmem {
 struct Bars {
   uint64_t work_full[2], work_empty[2], q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_empty[2], drain[2];  // [row tile][half of a step]
+  uint64_t twin_full, twin_empty;  // the second twin's maxima and sums
 };
 constexpr int kWorkReaders = 8 + 4 + 2;  // warps
 
@@ -205,9 +211,10 @@ __device__ __forceinline__ int token_in(const AttnParams &p, int row) { return t
 
 // ---------------------------------------------------------------- what a block works on
 // Items are 256 query rows of one key head of one sequence.
-// An item costs its key steps and kItemCost more (queries in, output out, the pipeline's start:
-// measured at about two steps).
-constexpr int kItemCost = 2;
+// An item costs its key steps and kItemCost more (queries in, output out, the pipeline's start). With
+// 2, 3, 4, 6, 8 the prompt of 8192 tokens takes 616, 552, 546, 550, 561 us, the drafted tokens 39.5,
+// 40.8, 38.8, 39.3, 39.7, the window 91.1, 88.2, 88.4, 90.2, 90.3; the cross attention does not care.
+constexpr int kItemCost = 4;
 struct Range {
   int q0, rows, kv_len, first_pos, row0;
   int lo[2], hi[2];  // key steps of each row tile; lo >= hi: none
@@ -220,6 +227,7 @@ struct Work {
   ItemParts parts;
 };
 
+template <bool TWIN>
 __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt) {
   Range w;
   const int q1 = __ldg(p.b.cu_q + seq + 1);
@@ -233,13 +241,13 @@ __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     int k_lo = 0, k_hi = reach;
-    const int last = min(w.rows, (t + 1) * kRows) - 1;
+    const int base = TWIN ? 0 : t * kRows, last = min(w.rows, base + kRows) - 1;
     if (p.causal) {
       k_hi = min(k_hi, w.first_pos + token_in(p, w.row0 + max(last, 0)) + 1);
-      if (p.window > 0) k_lo = max(0, w.first_pos + token_in(p, w.row0 + t * kRows) - p.window + 1);
+      if (p.window > 0) k_lo = max(0, w.first_pos + token_in(p, w.row0 + base) - p.window + 1);
     }
     w.lo[t] = k_lo / kKeys;
-    w.hi[t] = last >= t * kRows ? (max(k_hi, 0) + kKeys - 1) / kKeys : 0;
+    w.hi[t] = last >= base ? (max(k_hi, 0) + kKeys - 1) / kKeys : 0;
     if (w.lo[t] < w.hi[t]) w.begin = min(w.begin, w.lo[t]), w.end = max(w.end, w.hi[t]);
   }
   if (w.end == 0) w.begin = 0;
@@ -365,6 +373,7 @@ __device__ __forceinline__ void st256(void *p, const uint32_t *v) {
 }
 
 // The share's next segment (rows 0: none is left). One thread; the walk's state stays in `sh`.
+template <bool TWIN>
 __device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles, Share &sh, Work &out) {
   const int heads = p.c.kv_heads;
   const long long at = sh.cut[0];
@@ -375,7 +384,7 @@ __device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles,
   long long first = sh.first;
   for (;; ++sh.entry) {  // entries without rows have no steps
     x.seq = sh.entry / row_tiles;
-    x.r = item_range(p, x.seq, sh.entry % row_tiles);
+    x.r = item_range<TWIN>(p, x.seq, sh.entry % row_tiles);
     cost = x.r.cost();
     if (at < first + (long long)cost * heads) break;
     first += (long long)cost * heads;
@@ -390,7 +399,10 @@ __device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles,
     const int until = x.r.begin + (int)(to - p0) - kItemCost;
     x.r.begin = from, x.r.end = until;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) x.r.lo[t] = max(x.r.lo[t], from), x.r.hi[t] = min(x.r.hi[t], until);
+    for (int t = 0; t < 2; ++t) {
+      x.r.lo[t] = max(x.r.lo[t], from), x.r.hi[t] = min(x.r.hi[t], until);
+      if (TWIN) x.r.lo[t] += (x.r.lo[t] ^ t) & 1, x.r.hi[t] -= ((x.r.hi[t] - 1) ^ t) & 1;
+    }
   }
   sh.cut[0] = to;
   out = x;
@@ -400,7 +412,7 @@ __device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles,
 // all loads in flight at once. The row's largest value moves to [2^12, 2^13): exact in float16 down
 // to 2^-36 of it. The sign of the score's factor goes into the query, so that maxima stay maxima.
 template <int D, bool MX>
-__device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w, int t, int row_base, int lane, uint32_t q_tile,
+__device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w, int first, int row_base, int lane, uint32_t q_tile,
                                              float *coef) {
   constexpr int L = D / 16, RW = 32 / L, N = 32 / RW;
   const int sub = lane / L, chunk = lane % L * 2;
@@ -408,7 +420,7 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w,
   uint4 v[N][2];
 #pragma unroll
   for (int x = 0; x < N; ++x) {
-    const int r = t * kRows + row_base + x * RW + sub, row = w.r.row0 + r;
+    const int r = first + row_base + x * RW + sub, row = w.r.row0 + r;
     const int at = token_in(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
     v[x][0] = v[x][1] = make_uint4(0, 0, 0, 0);
     if (r < w.r.rows && token >= 0 && token < p.b.tokens) {
@@ -442,7 +454,7 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w,
   __syncwarp();
 }
 
-template <int D, bool MX>
+template <int D, bool MX, bool TWIN>
 __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_constant__ AttnParams p, int row_tiles) {
   using M = TileSmem<D>;
   constexpr KvLayout G = kv_group(D, MX ? 1 : 0);
@@ -451,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
   __shared__ Share share;
   __shared__ Work ring[2];
   __shared__ long long warp_sums[kThreads / 32];
+  __shared__ float2 twin_ml[TWIN ? kRows : 1];  // the second twin's maxima and sums
   __shared__ float row_coef[2 * kRows];  // score factor of each row of the segment
   __shared__ uint32_t tmem_slot;
   __shared__ volatile uint32_t abort_flag;
@@ -479,10 +492,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       kv_mbar_init(bar(bars.o_empty[i]), 4);
       kv_mbar_init(bar(bars.drain[i]), 1);
     }
+    kv_mbar_init(bar(bars.twin_full), 4);
+    kv_mbar_init(bar(bars.twin_empty), 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   find_share<kThreads, kItemCost>((long long)p.b.n_seq * row_tiles, p.c.kv_heads, kItemCost + 2, &share, warp_sums,
-                                  [&](long long e) { return item_range(p, (int)e / row_tiles, (int)e % row_tiles).cost(); });
+                                  [&](long long e) { return item_range<TWIN>(p, (int)e / row_tiles, (int)e % row_tiles).cost(); });
   if (share.cut[0] >= share.cut[1]) return;
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem_u32(&tmem_slot)), "r"(kTmemCols));
@@ -499,11 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 tensor-memory lanes
     const uint32_t s_tm = tmem + lanes + t * 128, o_tm = tmem + lanes + 256 + t * 128;
+    const int first = TWIN ? 0 : t * kRows, stride = TWIN ? 2 : 1;  // this tile's rows and key steps
     int n = 0, steps = 0;  // steps of this row tile, key steps of all segments so far
     auto queries = [&](int seg) {
       const Work &x = ring[seg & 1];
       if ((t ? x.r.lo[1] : x.r.lo[0]) >= (t ? x.r.hi[1] : x.r.hi[0])) return;
-      load_queries<D, MX>(p, x, t, 32 * (warp & 3), lane, base + M::kQ + t * M::kTile, row_coef + t * kRows);
+      load_queries<D, MX>(p, x, first, 32 * (warp & 3), lane, base + M::kQ + t * M::kTile, row_coef + t * kRows);
       mbar_arrive_warp(bar(bars.q_full[t]));
     };
     bool more = get_work(bars, ring, 0, limit, &abort_flag);
@@ -513,15 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       const int lo = t ? w.r.lo[1] : w.r.lo[0], hi = t ? w.r.hi[1] : w.r.hi[0];
       const int step0 = steps - w.r.begin;
       steps += w.r.end - w.r.begin;
-      const int kv_len = w.r.kv_len, pos = w.r.first_pos + token_in(p, w.r.row0 + t * kRows + r);
+      const int kv_len = w.r.kv_len, pos = w.r.first_pos + token_in(p, w.r.row0 + first + r);
       const int see_hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
       const int see_lo = p.causal && p.window > 0 ? pos - p.window : -1;
-      const int last = max(min(w.r.rows, (t + 1) * kRows) - 1, 0);
-      const int tile_lo = w.r.first_pos + token_in(p, w.r.row0 + t * kRows), tile_hi = w.r.first_pos + token_in(p, w.r.row0 + last);
+      const int last = max(min(w.r.rows, first + kRows) - 1, 0);
+      const int tile_lo = w.r.first_pos + token_in(p, w.r.row0 + first), tile_hi = w.r.first_pos + token_in(p, w.r.row0 + last);
       const float c = row_coef[t * kRows + r];  // of this warp's making; unused without steps
       float m = -INFINITY, l = 0.f;  // m: reference of the exponentials, in units of log2
       bool ok = true;
-      for (int i = lo; i < hi && ok; ++i, ++n) {
+      for (int i = lo; i < hi && ok; i += stride, ++n) {
         const int key0 = i * kKeys;
         uint32_t groups = 0x03030303u;
         bool whole = true;
@@ -611,14 +627,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       // every score product of this segment has arrived: its queries may go
       more = get_work(bars, ring, seg + 1, limit, &abort_flag);
       if (more) queries(seg + 1);
-      if (t * kRows >= w.r.rows) continue;
+      if (first >= w.r.rows) continue;
       const bool any = lo < hi;
       if (any) {
         if (!mbar_wait_warp(bar(bars.pv_done[t][1]), (n - 1) & 1, limit, &abort_flag)) break;
         tc_fence_after();
       }
-      const int row = w.r.row0 + t * kRows + r;  // row of the sequence's key head
-      const bool live = t * kRows + r < w.r.rows;
+      // The second twin hands maxima and sums over; its O is read where it lies, by the warp whose
+      // tensor-memory lanes, and so whose rows, are the same.
+      float f0 = 1.f, f1 = 0.f;
+      bool other = false;
+      if (TWIN) {
+        if (t) {
+          if (seg && !mbar_wait_warp(bar(bars.twin_empty), (seg - 1) & 1, limit, &abort_flag)) break;
+          twin_ml[r] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive_warp(bar(bars.twin_full));
+          continue;
+        }
+        other = w.r.lo[1] < w.r.hi[1];
+        if (!mbar_wait_warp(bar(bars.twin_full), seg & 1, limit, &abort_flag)) break;
+        tc_fence_after();
+        const float2 ml = twin_ml[r];
+        mbar_arrive_warp(bar(bars.twin_empty));
+        const float both = fmaxf(m, ml.x), ref = both == -INFINITY ? 0.f : both;
+        f0 = kv_ex2(m - ref), f1 = kv_ex2(ml.x - ref);
+        l = l * f0 + ml.y * f1, m = both;
+      }
+      const int row = w.r.row0 + first + r;  // row of the sequence's key head
+      const bool live = first + r < w.r.rows;
       const int at = token_in(p, row), token = w.r.q0 + at, head = w.kh * p.group + row - at * p.group;
       const bool real = live && token >= 0 && token < p.b.tokens;
       const float v_scale = MX || !p.c.v_scale ? 1.f : __ldg(p.c.v_scale + w.kh);
@@ -646,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       };
       const float inv = l == 0.f ? 0.f : v_scale / l;
       // parts: [block][first or not][row tile]: O as [4 elements][row], then m and l by row
-      const int tiles = p.b.max_q * p.group > kRows ? 2 : 1;
+      const int tiles = TWIN ? 1 : 2;
       float *const parts = reinterpret_cast<float *>(p.workspace + kAttnCounterBytes);
       auto part_at = [&](int j) {
         return parts + (((size_t)(w.parts.owner + j) * 2 + (j == 0 ? 1 : 0)) * tiles + t) * kRows * (D + 2);
@@ -662,7 +699,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
 #pragma unroll
           for (int j = 0; j < 32; ++j) ov[j] = 0u;
         }
-        const float *o = reinterpret_cast<const float *>(ov);
+        float *o = reinterpret_cast<float *>(ov);
+        if (TWIN) {
+          uint32_t tv[32];
+          if (other) {
+            tm_ld32(o_tm + 128 + 32 * x, tv);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) tv[j] = 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fmaf(o[j], f0, __uint_as_float(tv[j]) * f1);
+        }
         if (w.parts.count == 1) put(x, o, inv);
         else if (live) {
 #pragma unroll
@@ -674,6 +723,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       if (any) {
         tc_fence_before();
         mbar_arrive_warp(bar(bars.o_empty[t]));
+      }
+      if (other) {
+        tc_fence_before();
+        mbar_arrive_warp(bar(bars.o_empty[1]));
       }
       if (w.parts.count == 1) {
         put_lse(m, l);
@@ -815,6 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       tc_fence_after();
     };
     const uint32_t qd = desc_low(16, base + M::kQ + t * M::kTile), o_tm = tmem + 256 + t * 128, s_tm = tmem + t * 128;
+    const int skip = TWIN ? 1 : 0;  // every second step is the other tile's
     uint32_t q_n = 0, p_n = 0, items = 0;  // parities of the queries and of the products; there was an item
     int n0 = 0;                            // key steps of all segments
     for (int seg = 0; ok && get_work(bars, ring, seg, limit, &abort_flag); ++seg) {
@@ -824,7 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       done_work(bars, seg);
       for (int i = begin - 1; ok && i < end; ++i) {
         const int n = n0 + i - begin;
-        const bool more = i + 1 < end, products = i >= lo && i < hi, scores = i + 1 >= lo && i + 1 < hi;
+        const bool more = i + 1 < end, products = i >= lo && i < hi && !((i ^ t) & skip),
+                   scores = i + 1 >= lo && i + 1 < hi && !((i + 1 ^ t) & skip);
         // a tile without keys here waits too: both warps hand every operand tile back, once a step
         if (more) wait(bars.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
         if (i >= begin) wait(bars.v_full[n & 1], (n >> 1) & 1);
@@ -882,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
     if (warp == 14 && lane == 0) {
       for (int seg = 0;; ++seg) {
         if (seg >= 2 && !mbar_wait(bar(bars.work_empty[seg & 1]), ((seg >> 1) - 1) & 1, limit, &abort_flag)) break;
-        next_segment(p, row_tiles, share, ring[seg & 1]);
+        next_segment<TWIN>(p, row_tiles, share, ring[seg & 1]);
         const bool end = ring[seg & 1].r.rows <= 0;
         mbar_arrive(bar(bars.work_full[seg & 1]));
         if (end) break;
@@ -901,9 +956,9 @@ int row_tiles(const AttnParams &p) {
   return (int)(((long long)p.b.max_q * p.group + 2 * kRows - 1) / (2 * kRows));
 }
 
-template <int D, bool MX>
-cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
-  auto kernel = attn_tiles_kernel<D, MX>;
+template <int D, bool MX, bool TWIN>
+cudaError_t launch_t(const AttnParams &p, cudaStream_t st) {
+  auto kernel = attn_tiles_kernel<D, MX, TWIN>;
   if ((long long)p.b.n_seq * row_tiles(p) > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   static SmemOnce once;
   if (cudaError_t e = once.set(kernel, TileSmem<D>::kTotal)) return e;
@@ -911,10 +966,17 @@ cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+bool is_twin(const AttnParams &p) { return (long long)p.b.max_q * p.group <= kRows; }
+
+template <int D, bool MX>
+cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
+  return is_twin(p) ? launch_t<D, MX, true>(p, st) : launch_t<D, MX, false>(p, st);
+}
+
 }  // namespace
 
 size_t attention_tiles_workspace(const AttnParams &p, int d) {
-  const int tiles = (long long)p.b.max_q * p.group > kRows ? 2 : 1;  // row tiles that a part can have
+  const int tiles = is_twin(p) ? 1 : 2;  // row tiles that a part can have
   return kAttnCounterBytes + (size_t)sm_count() * 2 * tiles * kRows * (d + 2) * sizeof(float);
 }
 

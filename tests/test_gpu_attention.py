@@ -187,6 +187,60 @@ def test_many_sequences_of_uneven_length():
     run(S, st, new, 2)
 
 
+# 33 to 128 query rows of a key head: two tiles of a block share them, each with every second step of
+# 128 keys, so the number of steps, and which one an item or a cut begins with, matter
+@pytest.mark.parametrize("fmt,d", [("nvfp4", 128), ("mxfp4", 64)])
+@pytest.mark.parametrize("group,new", [(1, 33), (7, 5), (4, 32), (16, 8), (40, 3), (128, 1)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 100), (True, 300), (False, 0)])
+def test_one_row_tile(fmt, d, group, new, causal, window):
+    S = require_gpu()
+    lengths = [new, 127 + new, 128 + new, 129 + new, 256 + new, 257 + new, 384 + new, 513 + new, 1700, 5]
+    news = [new] * 9 + [min(new, 5)]
+    st = Setup(S, np.random.default_rng(group + new), lengths, 2, d, fmt, 32).fill()
+    run(S, st, news, group, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("lengths", [[128 * 300 + 77], [128 * 150 + 1, 40], [60, 128 * 149]])
+def test_one_row_tile_cut_between_blocks(lengths):
+    S = require_gpu()
+    st = Setup(S, np.random.default_rng(3), lengths, 1, 128, "nvfp4", 64).fill()
+    run(S, st, [9] * len(lengths), 8)
+    run(S, st, [9] * len(lengths), 8, q_mul=30.0)
+
+
+def test_one_row_tile_with_a_row_that_is_not_a_number():
+    """Its row alone; and where only one of the two tiles sees keys."""
+    S = require_gpu()
+    rng = np.random.default_rng(11)
+    for length, window in ((100, 0), (400, 0), (400, 60)):
+        st = Setup(S, rng, [length], 2, 128, "nvfp4", 16).fill()
+        q, x = bf16(rng, 20, 8, 128)
+        q[3, 5, 7] = float("nan")
+        y, lse = S.sharq_attention(q, st.cache, st.batch([20]), window=window, return_lse=True)
+        assert torch.isnan(y[3, 5]).all() and torch.isnan(lse[3, 5])
+        k, v = st.kv(0, length)
+        ref = K.attention(np.nan_to_num(q.double().cpu().numpy()), k, v, length - 20, True, window, 128 ** -0.5)
+        for got, want in ((y, 0), (lse, 1)):
+            got[3, 5] = torch.as_tensor(ref[want][3, 5]).to(got)
+        check_attention(y, lse, ref)
+
+
+def test_one_row_tile_across_missing_pages():
+    S = require_gpu()
+    rng = np.random.default_rng(12)
+    st = Setup(S, rng, [700, 300], 2, 64, "mxfp4", 16).fill()
+    table = st.table.copy()
+    table[0, 8:16] = -1   # the second step of 128 keys and some of the others
+    table[0, 20] = table[1, 0] = st.num_pages
+    q, x = bf16(rng, 50, 4, 64)
+    y, lse = S.sharq_attention(q, st.cache, st.batch([25, 25], table=table), return_lse=True)
+    for b, (length, gone) in enumerate(((700, [*range(8, 16), 20]), (300, [0]))):
+        k, v = st.kv(b, length)
+        place = ~np.isin(np.arange(length) // 16, gone)
+        rows = slice(25 * b, 25 * b + 25)
+        check_attention(y[rows], lse[rows], K.attention(x[rows], k, v, length - 25, True, 0, 64 ** -0.5, place))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("new", [1, 3, 70])
 def test_buffers_at_their_least_alignment(new, d):
