@@ -34,7 +34,10 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTile = 32;   // keys per step of a warp: two groups of the cache
 constexpr int kStagesA = 2;  // tiles of a warp's ring: the next one loads while one is used (a third gained nothing)
-constexpr int kItemCost = 8;  // what an item costs besides its tiles (queries, joining eight warps), in tiles
+// What an item costs besides its tiles (queries, joining eight warps), in tiles. With 8, 12, 16, 20, 32:
+// 64 uneven contexts 78.4, 73.5, 72.6, 73.0, 74.8 us, two of 128K tokens 66.1, 65.4, 64.8, 64.8, 65.0,
+// 128 of 200 to 1500 tokens 51.8, 46.5, 46.8, 48.0, 48.5.
+constexpr int kItemCost = 16;
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
