@@ -38,6 +38,10 @@ constexpr int kStagesA = 2;  // tiles of a warp's ring: the next one loads while
 // 64 uneven contexts 78.4, 73.5, 72.6, 73.0, 74.8 us, two of 128K tokens 66.1, 65.4, 64.8, 64.8, 65.0,
 // 128 of 200 to 1500 tokens 51.8, 46.5, 46.8, 48.0, 48.5.
 constexpr int kItemCost = 16;
+constexpr int kJoin = 16;  // parts that one block joins
+// counters: an item's by its first block, then a group's by the block and the slot of its first part
+constexpr int kGroupCounter = 512;
+static_assert(4 * (kGroupCounter + 2 * kGroupCounter) <= kAttnCounterBytes, "counters of 512 blocks");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -500,29 +504,42 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       }
     }
     if (parts.count > 1) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + parts.owner;
-        last_part = atomicAdd(counter, 1u) + 1 == (uint32_t)parts.count;
-        if (last_part) *counter = 0;  // ready for the next call
-      }
-      __syncthreads();
-      if (last_part) {
+      // The last block to arrive joins. More than two groups of kJoin parts (a few long contexts) join
+      // in two levels, each group into its first part's place: one block alone would read up to 148
+      // or 296 parts, and took longer than all blocks' keys.
+      auto arrive_last = [&](int counter, int members) {
         __threadfence();
-        for (int idx = threadIdx.x; idx < rows * F4; idx += kWarps * 32) {
-          const int row = idx / F4, i4 = idx % F4;
-          // eight parts' loads are in flight at once; references move from eight to eight
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          uint32_t *c = reinterpret_cast<uint32_t *>(p.workspace) + counter;
+          last_part = atomicAdd(c, 1u) + 1 == (uint32_t)members;
+          if (last_part) *c = 0;  // ready for the next call
+        }
+        __syncthreads();
+        const bool last = last_part != 0;
+        if (last) __threadfence();
+        return last;
+      };
+      // parts j0, j0 + step, ... below `end`, in the order of the keys
+      bool whole = parts.count <= 2 * kJoin;
+      int j0 = whole ? 0 : parts.index / kJoin * kJoin, step = 1, end = whole ? parts.count : min(j0 + kJoin, parts.count);
+      bool last = whole ? arrive_last(parts.owner, parts.count)
+                        : arrive_last(kGroupCounter + 2 * (parts.owner + j0) + (j0 == 0 ? 1 : 0), end - j0);
+      while (last) {
+        // eight parts' loads are in flight at once, references move from eight to eight
+        for (int base = 0; base < rows * F4; base += kWarps * 32) {  // whole rows at a time
+          const int idx = base + threadIdx.x, row = idx / F4, i4 = idx % F4;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           float mm = -INFINITY, ll = 0.f;
-          for (int j0 = 0; j0 < parts.count; j0 += 8) {
+          for (int ja = j0; ja < end && row < rows; ja += 8 * step) {
             float2 ml[8];
             float4 u[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const bool some = j0 + j < parts.count;
-              ml[j] = some ? __ldcg(reinterpret_cast<const float2 *>(part_at(j0 + j) + C::R * D) + row) : make_float2(-INFINITY, 0.f);
-              u[j] = some ? __ldcg(reinterpret_cast<const float4 *>(part_at(j0 + j)) + idx) : make_float4(0.f, 0.f, 0.f, 0.f);
+              const bool some = ja + j * step < end;
+              const float *src = part_at(some ? ja + j * step : ja);
+              ml[j] = some ? __ldcg(reinterpret_cast<const float2 *>(src + C::R * D) + row) : make_float2(-INFINITY, 0.f);
+              u[j] = some ? __ldcg(reinterpret_cast<const float4 *>(src) + idx) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float top = mm;
 #pragma unroll
@@ -537,8 +554,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
               v.x = fmaf(u[j].x, f, v.x), v.y = fmaf(u[j].y, f, v.y), v.z = fmaf(u[j].z, f, v.z), v.w = fmaf(u[j].w, f, v.w);
             }
           }
-          put(row, i4, v, mm, ll);
+          if (whole) {
+            if (row < rows) put(row, i4, v, mm, ll);
+            continue;
+          }
+          __syncthreads();  // every thread of a row has read the m and l that are overwritten
+          if (row >= rows) continue;
+          __stcg(reinterpret_cast<float4 *>(part_at(j0)) + idx, v);
+          if (i4 == 0) __stcg(reinterpret_cast<float2 *>(part_at(j0) + C::R * D) + row, make_float2(mm, ll));
         }
+        if (whole) break;
+        last = arrive_last(parts.owner, (parts.count + kJoin - 1) / kJoin);
+        whole = true, j0 = 0, step = kJoin, end = parts.count;
       }
     }
     // the next segment's copies overwrite what was just read

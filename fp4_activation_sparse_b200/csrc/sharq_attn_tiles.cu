@@ -65,6 +65,10 @@ constexpr int kKeys = 128;  // keys of a step
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;  // S of tile t, half h at 128 t + 64 h (P over its first 32); O at 256 + 128 t
 constexpr int kValidRing = 4;
+// counters, eight (one per softmax warp) each: an item's by its first block, then a group's by the
+// block and the slot of its first part
+constexpr int kGroupCounter = 256;
+static_assert(4 * 8 * (kGroupCounter + 2 * kGroupCounter) <= kAttnCounterBytes, "counters of 256 blocks");
 
 template <int D>
 struct TileSmem {
@@ -733,68 +737,93 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         continue;
       }
       if (live) __stcg(reinterpret_cast<float2 *>(mine + D * kRows) + r, make_float2(m, l));
-      // Each warp joins its own 32 rows with the same warp of the item's other parts: a barrier among the
-      // four would wait without limit for a warp that gave up.
-      __threadfence();
-      __syncwarp();
-      uint32_t arrived_last = 0;
-      if (lane == 0) {
-        uint32_t *counter = reinterpret_cast<uint32_t *>(p.workspace) + 8 * w.parts.owner + warp;
-        arrived_last = atomicAdd(counter, 1u) + 1 == (uint32_t)w.parts.count;
-        if (arrived_last) *counter = 0;  // ready for the next call
-      }
-      if (!__shfl_sync(0xFFFFFFFFu, arrived_last, 0)) continue;
-      __threadfence();
-      if (!live) continue;
-      // Latency is most of the joining: the first four parts' (more are rare) m and l are loaded at once,
-      // O by two parts. (Four parts of O at once took registers that the prompt's loop missed: 1 % there,
-      // for 1 % of the drafted tokens.)
-      auto ml_at = [&](int j) { return __ldcg(reinterpret_cast<const float2 *>(part_at(j) + D * kRows) + r); };
-      float2 ml[4];
+      // Each warp joins its own 32 rows with the same warp of the item's other parts (a barrier among the
+      // four would wait without limit for a warp that gave up), the last one to arrive all of them.
+      // More than eight parts (few long contexts) join in two levels, each group into its first part's
+      // place: one warp alone would take longer than all blocks' keys.
+      auto arrive_last = [&](int counter, int members) {
+        __threadfence();
+        __syncwarp();
+        uint32_t is_last = 0;
+        if (lane == 0) {
+          uint32_t *c = reinterpret_cast<uint32_t *>(p.workspace) + 8 * counter + warp;
+          is_last = atomicAdd(c, 1u) + 1 == (uint32_t)members;
+          if (is_last) *c = 0;  // ready for the next call
+        }
+        is_last = __shfl_sync(0xFFFFFFFFu, is_last, 0);
+        if (is_last) __threadfence();
+        return is_last != 0;
+      };
+      const int count = w.parts.count, owner = w.parts.owner;
+      int size = 4;  // parts of a group: about as many as groups
+      while (size * size < count) ++size;
+      bool whole = count <= 8;
+      int j0 = whole ? 0 : w.parts.index / size * size, step = 1, n_join = whole ? count : min(size, count - j0);
+      bool joins = whole ? arrive_last(owner, count) : arrive_last(kGroupCounter + 2 * (owner + j0) + (j0 == 0 ? 1 : 0), n_join);
+      while (joins) {
+        auto joined = [&](int j) { return part_at(j0 + j * step); };
+        auto ml_at = [&](int j) { return __ldcg(reinterpret_cast<const float2 *>(joined(j) + D * kRows) + r); };
+        if (live) {
+          // Latency is most of the joining: the first four parts' m and l are loaded at once, O by four parts
+          // between twins, by two else (four take registers that the prompt's loop misses: 1 % there).
+          constexpr int kAtOnce = TWIN ? 4 : 2;
+          float2 ml[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ml[j] = j < w.parts.count ? ml_at(j) : make_float2(-INFINITY, 0.f);
-      float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), ll = 0.f, f[4];
-      for (int j = 4; j < w.parts.count; ++j) mm = fmaxf(mm, ml_at(j).x);
-      const float ref = mm == -INFINITY ? 0.f : mm;
+          for (int j = 0; j < 4; ++j) ml[j] = j < n_join ? ml_at(j) : make_float2(-INFINITY, 0.f);
+          float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), ll = 0.f;
+#pragma unroll 4
+          for (int j = 4; j < n_join; ++j) mm = fmaxf(mm, ml_at(j).x);
+          const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = kv_ex2(ml[j].x - ref), ll += ml[j].y * f[j];
-      for (int j = 4; j < w.parts.count; ++j) {
-        const float2 v = ml_at(j);
-        ll += v.y * kv_ex2(v.x - ref);
-      }
-      const float inv_all = ll == 0.f ? 0.f : v_scale / ll;
-#pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
-        auto o_at = [&](int j, int e) { return __ldcg(reinterpret_cast<const float4 *>(part_at(j)) + (8 * x + e) * kRows + r); };
-        float o[32];
-        auto add = [&](const float4 (&v)[8], float g) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            o[4 * e] = fmaf(v[e].x, g, o[4 * e]), o[4 * e + 1] = fmaf(v[e].y, g, o[4 * e + 1]);
-            o[4 * e + 2] = fmaf(v[e].z, g, o[4 * e + 2]), o[4 * e + 3] = fmaf(v[e].w, g, o[4 * e + 3]);
+          for (int j = 0; j < 4; ++j) ml[j].x = kv_ex2(ml[j].x - ref), ll += ml[j].y * ml[j].x;
+#pragma unroll 4
+          for (int j = 4; j < n_join; ++j) {
+            const float2 v = ml_at(j);
+            ll += v.y * kv_ex2(v.x - ref);
           }
-        };
-        float4 v[2][8];
+          const float inv_all = ll == 0.f ? 0.f : v_scale / ll;
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            float o[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+            for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < n_join; j += kAtOnce) {
+              float4 v[kAtOnce][8];
+              float f[kAtOnce];
 #pragma unroll
-        for (int j0 = 0; j0 < 4; j0 += 2) {
+              for (int y = 0; y < kAtOnce; ++y) {
+                const bool some = j + y < n_join;
+                const float4 *src = reinterpret_cast<const float4 *>(joined(j + (some ? y : 0))) + 8 * x * kRows + r;
+                f[y] = !some ? 0.f : j == 0 ? ml[y].x : j == 2 ? ml[(2 + y) & 3].x : kv_ex2(ml_at(j + y).x - ref);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+                for (int e = 0; e < 8; ++e) v[y][e] = some ? __ldcg(src + e * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = j0 + j < w.parts.count ? o_at(j0 + j, e) : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int y = 0; y < kAtOnce; ++y)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) add(v[j], f[j0 + j]);
+                for (int e = 0; e < 8; ++e) {
+                  o[4 * e] = fmaf(v[y][e].x, f[y], o[4 * e]), o[4 * e + 1] = fmaf(v[y][e].y, f[y], o[4 * e + 1]);
+                  o[4 * e + 2] = fmaf(v[y][e].z, f[y], o[4 * e + 2]), o[4 * e + 3] = fmaf(v[y][e].w, f[y], o[4 * e + 3]);
+                }
+            }
+            if (whole) {
+              put(x, o, inv_all);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                __stcg(reinterpret_cast<float4 *>(joined(0)) + (8 * x + e) * kRows + r,
+                       make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+            }
+          }
+          if (whole) put_lse(mm, ll);
+          else __stcg(reinterpret_cast<float2 *>(joined(0) + D * kRows) + r, make_float2(mm, ll));
         }
-        for (int j = 4; j < w.parts.count; ++j) {
-          const float g = kv_ex2(ml_at(j).x - ref);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[0][e] = o_at(j, e);
-          add(v[0], g);
-        }
-        put(x, o, inv_all);
+        if (whole) break;
+        __syncwarp();
+        joins = arrive_last(owner, (count + size - 1) / size);
+        whole = true, j0 = 0, step = size, n_join = (count + size - 1) / size;
       }
-      put_lse(mm, ll);
     }
     tc_fence_before();
   } else if (warp < 12) {

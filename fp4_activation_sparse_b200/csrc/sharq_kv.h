@@ -113,7 +113,7 @@ cudaError_t launch_kv_append(const AppendParams &p, int d, int fmt, cudaStream_t
 cudaError_t launch_kv_read(const ReadParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t launch_attention(const AttnParams &p, int d, int fmt, cudaStream_t st);
 // The attention workspace: counters (zero between calls), then parts of cut items.
-constexpr int kAttnCounterBytes = 8192;
+constexpr int kAttnCounterBytes = 32768;
 size_t attention_tiles_workspace(const AttnParams &p, int d);
 cudaError_t launch_attention_tiles(const AttnParams &p, int d, int fmt, cudaStream_t st);
 cudaError_t read_and_clear_attn_status(uint32_t *status);

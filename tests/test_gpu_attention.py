@@ -208,6 +208,20 @@ def test_one_row_tile_cut_between_blocks(lengths):
     run(S, st, [9] * len(lengths), 8, q_mul=30.0)
 
 
+@pytest.mark.parametrize("group,new,length", [(1, 1, 60011), (4, 1, 9999), (12, 1, 50000), (32, 1, 40000), (7, 5, 50000),
+                                              (40, 5, 30000), (4, 3, 2700)])
+@pytest.mark.parametrize("heads,d,fmt", [(1, 128, "nvfp4"), (2, 64, "mxfp4")])
+def test_items_of_many_parts(group, new, length, heads, d, fmt):
+    """One context over all blocks: up to hundreds of parts, joined in two levels; then the same call
+    again, with the counters as the first one left them."""
+    S = require_gpu()
+    st = Setup(S, np.random.default_rng(group), [length], heads, d, fmt, 64).fill()
+    ws = S.alloc_attention_workspace(st.cache, st.batch([new]), group * heads)
+    q, y, lse = run(S, st, [new], group, workspace=ws)
+    y2, lse2 = S.sharq_attention(q, st.cache, st.batch([new]), return_lse=True, workspace=ws)
+    assert torch.equal(y, y2) and torch.equal(lse, lse2)
+
+
 def test_one_row_tile_with_a_row_that_is_not_a_number():
     """Its row alone; and where only one of the two tiles sees keys."""
     S = require_gpu()
