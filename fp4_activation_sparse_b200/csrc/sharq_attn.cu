@@ -18,8 +18,10 @@
 // looked up its page) keep the copying out of the instruction stream, which is the bound in
 // fact: about 640 instructions per 32 keys and warp, half of them turning codes into float16.
 //
-// Measured (32 query and 8 key heads of 128): 64 contexts of 33 to 8191 tokens 81 us, 3.8 TB/s; two of
-// 120 to 131 thousand 68 us, 4.0 TB/s; one of 777 tokens 10 us, which is latency.
+// Measured (32 query and 8 key heads of 128): 64 contexts of 33 to 8191 tokens 73 us, 4.2 TB/s; two of
+// 120 to 131 thousand 65 us, 4.2 TB/s; one of 777 tokens 9 us, which is latency. Tried without gain: more
+// warps (ten or twelve of them spill: 90 and 116 us for the 64 contexts), a third tile in the ring,
+// the score products split into two chains.
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
 #include "sharq_kv.h"
@@ -600,9 +602,10 @@ cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
 }  // namespace
 
 namespace {
-// 32 rows: what one block of the kernel above holds in registers. At 20 rows (16 contexts of 1500 to
-// 6000 tokens, 4 key heads) it takes 39 us and the 128-row tiles 45, at 32 rows both 41; at 8 rows of
-// one context of 50000 tokens 33 and 96.
+// 32 rows: what one block of the kernel above holds in registers. With 7 and 4 rows per token it takes, for
+// 16 contexts, 22, 34, 35 us at 14, 21, 28 rows where the 128-row tiles take 38, 38, 37, and 36, 60, 62 at
+// 16, 24, 32 rows where they take 65; for one context of 50000 tokens and one key head 18, 25, 29 at
+// 12, 24, 32 rows.
 bool use_tiles(const AttnParams &p) { return (long long)p.b.max_q * p.group > 32; }
 }  // namespace
 
