@@ -35,3 +35,8 @@ def test_timeout_is_reported_and_the_next_call_is_right(new):
         k, v = st.kv(b, lengths[b])
         rows = slice(b * new, (b + 1) * new)
         check_attention(y[rows], lse[rows], K.attention(x[rows], k, v, lengths[b] - new, True, 0, 128 ** -0.5))
+
+
+def test_timeout_with_one_row_tile():
+    """The two tiles of a block share the rows here, and one hands its sums to the other."""
+    test_timeout_is_reported_and_the_next_call_is_right(20)
