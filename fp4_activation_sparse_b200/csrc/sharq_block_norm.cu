@@ -4,11 +4,11 @@
 //   h  = bf16(r' * rstd(r') * pre_gamma)   (optional; rstd of r' as stored)
 // Bound by its bytes: y and r read once, r' and h written once, 8 bytes per element. One block
 // per row keeps the row in registers between the two reductions, so nothing is read twice.
-// Measured: 32760 x 5120 with a gate and both norms 208 us replayed on the same buffers (6.46 TB/s, a plain
-// copy's rate), 241 us on buffers that change; 288 us while the squares were added in float64 one by
-// one and a second barrier handed the sum back (the loop was then bound by its instructions).
-// Loading the next row ahead in a persistent block gained nothing. Few rows take a unit per thread
-// (16 x 4096: 3.0 us, against 5.1 with four).
+// Measured: 32760 x 5120 with a gate and both norms 227 us (5.9 TB/s). The squares are added in float64 one
+// by one, as the stand-alone norm does, so that a row's rstd is the same to the bit: 12 us of the 227
+// (with eight squares in float32 first, off by up to 4e-7, it took 215 us); as (x 2^-896)(x 2^896) from
+// four instructions per element instead of the three here it took 233. Loading the next row ahead in a
+// persistent block gained nothing. Few rows take a unit per thread (16 x 4096: 3.2 us, against 5.1 with four).
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
 #include "sharq_kv.h"
@@ -31,7 +31,19 @@ __device__ __forceinline__ float block_rstd(double ss, int k, float eps, double 
   __syncthreads();
   double t = 0.0;
   for (int i = 0; i < (int)(blockDim.x >> 5); ++i) t += red[i];
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(__double2float_rn(t * (1.0 / k)), eps)));
+  return __frcp_rn(__fsqrt_rn(__fadd_rn(__double2float_rn(__ddiv_rn(t, (double)k)), eps)));
+}
+
+// A thread's sum from the scaled one; once more with infinities and NaN where it may hold some.
+template <int U>
+__device__ __forceinline__ double unscaled(const uint4 (&v)[U], int units, double ss) {
+  if (ss < 1.0) return ss * 0x1p256;
+  ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    if (threadIdx.x + i * blockDim.x < units)
+      ss = add_squares_exact(v[i].w, add_squares_exact(v[i].z, add_squares_exact(v[i].y, add_squares_exact(v[i].x, ss))));
+  return ss;
 }
 
 // One row from its y and r in registers, U 16-byte units (8 bf16) per thread.
@@ -46,7 +58,8 @@ __device__ __forceinline__ void norm_row(const NormResidualParams &p, size_t row
   if (p.post_gamma) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (threadIdx.x + i * blockDim.x < units) ss += sum_squares(y[i]);
+      if (threadIdx.x + i * blockDim.x < units) ss = add_squares_scaled(y[i], ss);
+    ss = unscaled<U>(y, units, ss);
     rs = block_rstd(ss, p.k, p.eps, red[0]);
   }
   ss = 0.0;
@@ -75,11 +88,12 @@ __device__ __forceinline__ void norm_row(const NormResidualParams &p, size_t row
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         rw[j] = *reinterpret_cast<const uint32_t *>(&h);
       }
-      if (p.pre_gamma) ss += sum_squares(r[i]);
+      if (p.pre_gamma) ss = add_squares_scaled(r[i], ss);
       __stcs(reinterpret_cast<uint4 *>(p.residual_out + row * p.k) + u, r[i]);
     }
   }
   if (!p.pre_gamma) return;
+  ss = unscaled<U>(r, units, ss);
   rs = block_rstd(ss, p.k, p.eps, red[1]);
 #pragma unroll
   for (int i = 0; i < U; ++i) {

@@ -66,18 +66,19 @@ __device__ __forceinline__ uint32_t kv_scales2(uint32_t two) {
   return d;
 }
 
-// The sum of a unit's eight squares (exact products, seven float32 additions: 4e-7 of it at most) as
-// float64, in which everything further is summed. Where float32 could overflow or underflow the
-// squares are added in float64 one by one.
-__device__ __forceinline__ double sum_squares(const uint4 &v) {
-  float s = bf16lo(v.x) * bf16lo(v.x);
-  s = fmaf(bf16hi(v.x), bf16hi(v.x), s);
-  s = fmaf(bf16lo(v.y), bf16lo(v.y), s), s = fmaf(bf16hi(v.y), bf16hi(v.y), s);
-  s = fmaf(bf16lo(v.z), bf16lo(v.z), s), s = fmaf(bf16hi(v.z), bf16hi(v.z), s);
-  s = fmaf(bf16lo(v.w), bf16lo(v.w), s), s = fmaf(bf16hi(v.w), bf16hi(v.w), s);
-  if (s > 1e30f || s < 1e-25f)
-    return add_squares_exact(v.x, add_squares_exact(v.y, add_squares_exact(v.z, add_squares_exact(v.w, 0.0))));
-  return (double)s;
+// ss + a unit's eight squares * 2^-256, every addition in float64. An element's bits under an exponent field
+// raised by 768 are |x| * 2^-128 in two instructions (a square, 16 bits, is exact); a zero or subnormal
+// comes out below 2^-254 and cannot reach a float32 mean. Infinities and NaN are values of at least 1
+// there, and larger than any other: a sum below 1 has none.
+__device__ __forceinline__ double add_squares_scaled(const uint4 &v, double ss) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const double a = __hiloint2double((int)((w[i] << 13 & 0x0FFFE000u) | 0x30000000u), 0);
+    const double b = __hiloint2double((int)((w[i] >> 3 & 0x0FFFE000u) | 0x30000000u), 0);
+    ss = __fma_rn(b, b, __fma_rn(a, a, ss));
+  }
+  return ss;
 }
 
 // row / group for row < 2^32 / group (the entry point keeps to that)
