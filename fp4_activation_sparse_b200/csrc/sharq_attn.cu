@@ -375,20 +375,37 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
             for (int i = 0; i < KS; ++i) o[i][n][c] *= f, o[i][n][2 + c] *= f;
           }
       }
+      float most = 0.f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) most = max3abs(most, m[n][0], m[n][1]);
+      if (!__any_sync(0xFFFFFFFFu, most > 0x1p24f)) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float shift = m[n][c] == -INFINITY ? 0.f : -m[n][c];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < 2; ++c) {
+            const float shift = m[n][c] == -INFINITY ? 0.f : -m[n][c];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const float e = kv_ex2(fmaf(sc[h][n][2 * q + c], coef[n][c], shift));
-              sc[h][n][2 * q + c] = e;
-              l[n][c] += e;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float e = kv_ex2(fmaf(sc[h][n][2 * q + c], coef[n][c], shift));
+                sc[h][n][2 * q + c] = e;
+                l[n][c] += e;
+              }
+          }
+      } else {  // a column is far (see kv_is_far), or has seen nothing yet
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float shift = m[n][c] == -INFINITY ? 0.f : -m[n][c];
+              float &v = sc[x >> 1][n][2 * (x & 1) + c];
+              v = kv_ex2(kv_is_far(m[n][c]) ? __fadd_rn(__fmul_rn(v, coef[n][c]), shift) : fmaf(v, coef[n][c], shift));
+              l[n][c] += v;
             }
-        }
+      }
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

@@ -560,7 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
           }
           tc_wait_ld();
           float *s = reinterpret_cast<float *>(sr);
-          if (!whole) {
+          float by = c;  // what the scores are still to be multiplied by
+          const bool far = __any_sync(0xFFFFFFFFu, kv_is_far(m));
+          if (!whole || far) {
             const int top = see_hi - key0 - 64 * h, bottom = see_lo - key0 - 64 * h;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -570,10 +572,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
 #pragma unroll
               for (int j = 0; j < 32; ++j) s[32 * x + j] = see & (1u << j) ? s[32 * x + j] : -INFINITY;
             }
+            if (far) {
+              const float first = kv_is_far(m) ? c : 1.f;
+#pragma unroll
+              for (int j = 0; j < 64; ++j) s[j] = __fmul_rn(s[j], first);
+              by = kv_is_far(m) ? 1.f : c;
+            }
           }
           // The exponentials are formed against the reference at hand while the maximum is taken, and
           // once more in the rare half whose maximum is too far above it.
-          const uint64_t c2 = pack2(c, c);
+          const uint64_t c2 = pack2(by, by);
           uint32_t pr[32];
           float sum;
           auto exponentials = [&]() {
@@ -598,11 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
           for (int j = 0; j < 64; j += 8)
 #pragma unroll
             for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[j + 2 * x], s[j + 2 * x + 1]);
-          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+          const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * by;
           const bool grew = top > m + 8.f;
           if (__any_sync(0xFFFFFFFFu, grew)) {
             const float next = grew ? top : m;
             const float f = grew ? kv_ex2(m - next) : 1.f;  // 0 where nothing was seen before
+            const bool turned = __any_sync(0xFFFFFFFFu, kv_is_far(next) != kv_is_far(m));
             m = next;
             l *= f;
             exponentials();
@@ -619,6 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
                 for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * f);
                 tm_st32(o_tm + 32 * x, ov);
               }
+            }
+            if (__builtin_expect(turned, 0)) {  // the half once more, with these rows' scores multiplied first
+              --h;
+              continue;
             }
           }
           tm_st32(s_tm + 64 * h, pr);

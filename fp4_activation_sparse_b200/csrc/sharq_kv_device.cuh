@@ -81,6 +81,11 @@ __device__ __forceinline__ double add_squares_scaled(const uint4 &v, double ss) 
   return ss;
 }
 
+// Exponents are score * c - m in one rounding, m a rounded reference. Where |m| is beyond 2^24 that rounding of
+// m alone is worth powers of two (at 2^28 up to 2^16: past float16, or every key at zero). Such a row's
+// product is rounded by itself: the largest is then m exactly, and no other above it.
+__device__ __forceinline__ bool kv_is_far(float m) { return fabsf(m) > 0x1p24f && m != -INFINITY; }
+
 // row / group for row < 2^32 / group (the entry point keeps to that)
 __device__ __forceinline__ int token_of(int group, uint32_t group_inv, int row) {
   return group == 1 ? row : (int)__umulhi((uint32_t)row, group_inv);
