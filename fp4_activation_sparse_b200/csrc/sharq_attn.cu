@@ -132,7 +132,7 @@ __device__ __forceinline__ RowsRange rows_range(const AttnParams &p, int seq) {
   int k_lo = 0, k_hi = min(r.kv_len, p.b.max_pages << p.c.page_shift);  // no place behind the table
   if (p.causal) {
     k_hi = min(k_hi, r.first_pos + q_len);
-    if (p.window > 0) k_lo = max(0, r.first_pos - p.window + 1);
+    if (p.window > 0 && r.first_pos >= p.window) k_lo = r.first_pos - p.window + 1;
   }
   r.lo = k_lo / kTile;
   r.hi = (max(k_hi, 0) + kTile - 1) / kTile;
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       }
       // ---- masks
       const bool whole = valid == 3u && key0 + kTile <= kv_len &&
-                         (!p.causal || (key0 + kTile - 1 <= pos_lo && (p.window <= 0 || key0 > pos_hi - p.window)));
+                         (!p.causal || (key0 + kTile - 1 <= pos_lo && (p.window <= 0 || pos_hi - key0 < p.window)));
       if (!whole) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
           for (int c = 0; c < 2; ++c) {
             const int pos = first_pos + token_of(p.group, p.group_inv, n * 8 + 2 * t + c);
             const int hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
-            const int lo = p.causal && p.window > 0 ? pos - p.window : -1;
+            const int lo = p.causal && p.window > 0 && pos >= p.window ? pos - p.window : -1;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll

@@ -250,7 +250,8 @@ __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt
     const int base = TWIN ? 0 : t * kRows, last = min(w.rows, base + kRows) - 1;
     if (p.causal) {
       k_hi = min(k_hi, w.first_pos + token_in(p, w.row0 + max(last, 0)) + 1);
-      if (p.window > 0) k_lo = max(0, w.first_pos + token_in(p, w.row0 + base) - p.window + 1);
+      const int pos = w.first_pos + token_in(p, w.row0 + base);
+      if (p.window > 0 && pos >= p.window) k_lo = pos - p.window + 1;
     }
     w.lo[t] = k_lo / kKeys;
     w.hi[t] = last >= base ? (max(k_hi, 0) + kKeys - 1) / kKeys : 0;
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       steps += w.r.end - w.r.begin;
       const int kv_len = w.r.kv_len, pos = w.r.first_pos + token_in(p, w.r.row0 + first + r);
       const int see_hi = p.causal ? min(pos, kv_len - 1) : kv_len - 1;
-      const int see_lo = p.causal && p.window > 0 ? pos - p.window : -1;
+      const int see_lo = p.causal && p.window > 0 && pos >= p.window ? pos - p.window : -1;
       const int last = max(min(w.r.rows, first + kRows) - 1, 0);
       const int tile_lo = w.r.first_pos + token_in(p, w.r.row0 + first), tile_hi = w.r.first_pos + token_in(p, w.r.row0 + last);
       const float c = row_coef[t * kRows + r];  // of this warp's making; unused without steps
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
           if (h == 0) {
             groups = valid[(step0 + i) % kValidRing];
             whole = groups == 0x03030303u && key0 + kKeys <= kv_len &&
-                    (!p.causal || (key0 + kKeys - 1 <= tile_lo && (p.window <= 0 || key0 > tile_hi - p.window)));
+                    (!p.causal || (key0 + kKeys - 1 <= tile_lo && (p.window <= 0 || tile_hi - key0 < p.window)));
           }
           tc_wait_ld();
           float *s = reinterpret_cast<float *>(sr);
