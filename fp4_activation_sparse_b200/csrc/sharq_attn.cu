@@ -118,7 +118,7 @@ struct RowsKernel {
 
 // One sequence's query rows (all of them: the launch has at most R per key head) and key tiles.
 struct RowsRange {
-  int q0, rows, kv_len, first_pos, lo, hi;
+  int q0, rows, kv_len, first_pos, first_key, lo, hi;  // first_key: no query sees one before it
   __device__ __forceinline__ int cost() const { return rows <= 0 ? 0 : kItemCost + max(1, hi - lo); }
 };
 __device__ __forceinline__ RowsRange rows_range(const AttnParams &p, int seq) {
@@ -134,6 +134,7 @@ __device__ __forceinline__ RowsRange rows_range(const AttnParams &p, int seq) {
     k_hi = min(k_hi, r.first_pos + q_len);
     if (p.window > 0 && r.first_pos >= p.window) k_lo = r.first_pos - p.window + 1;
   }
+  r.first_key = k_lo;
   r.lo = k_lo / kTile;
   r.hi = (max(k_hi, 0) + kTile - 1) / kTile;
   return r;
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       if (at != p0) t_lo = w.lo + (int)(at - p0) - kItemCost;
     }
     at = to;
-    const int q0 = w.q0, rows = w.rows, kv_len = w.kv_len, first_pos = w.first_pos;
+    const int q0 = w.q0, rows = w.rows, kv_len = w.kv_len, first_pos = w.first_pos, first_key = w.first_key;
     const int pos_lo = first_pos, pos_hi = first_pos + token_of(p.group, p.group_inv, rows - 1);
 
     // ---- copies: 32 keys a stage, one bulk copy per group of 16
@@ -422,11 +423,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
         if (D == 128) lds128(vc + 512 + lane * 16, v[1]);
         constexpr int per_run = (MX ? 32 : 16) / (D / 8);  // runs that share a block: 1, 2 or 4
         uint32_t vs = lds32(st + h * G.bytes + G.v_scales + (g / per_run * 4 + t) * 4);
-        const int left = kv_len - (key0 + 16 * h);  // keys of the group that exist
-        if (left < 16) {  // scales of the others may be anything: zero keeps 0 * v from NaN
+        if (!whole) {  // scales of keys that no query sees may be anything: zero keeps 0 * v from NaN
+          const int from = first_key - (key0 + 16 * h), left = kv_len - (key0 + 16 * h);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (8 * (q >> 1) + 2 * t + (q & 1) >= left) vs &= ~(0xFFu << (8 * q));
+          for (int q = 0; q < 4; ++q) {
+            const int key = 8 * (q >> 1) + 2 * t + (q & 1);
+            if (key < from || key >= left) vs &= ~(0xFFu << (8 * q));
+          }
         }
         const uint32_t s0 = kv_scales2<MX>(vs & 0xFFFFu), s1 = kv_scales2<MX>(vs >> 16);
         uint32_t even[2][2], odd[2][2];  // [word][slot half]: nibbles of two keys of one element per byte

@@ -222,7 +222,7 @@ __device__ __forceinline__ int token_in(const AttnParams &p, int row) { return t
 // 40.8, 38.8, 39.3, 39.7, the window 91.1, 88.2, 88.4, 90.2, 90.3; the cross attention does not care.
 constexpr int kItemCost = 4;
 struct Range {
-  int q0, rows, kv_len, first_pos, row0;
+  int q0, rows, kv_len, first_pos, row0, first_key;  // first_key: no query of the item sees one before it
   int lo[2], hi[2];  // key steps of each row tile; lo >= hi: none
   int begin, end;    // of the item
   __device__ __forceinline__ int cost() const { return rows <= 0 ? 0 : kItemCost + max(1, end - begin); }
@@ -253,6 +253,7 @@ __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt
       const int pos = w.first_pos + token_in(p, w.row0 + base);
       if (p.window > 0 && pos >= p.window) k_lo = pos - p.window + 1;
     }
+    if (t == 0) w.first_key = k_lo;
     w.lo[t] = k_lo / kKeys;
     w.hi[t] = last >= base ? (max(k_hi, 0) + kKeys - 1) / kKeys : 0;
     if (w.lo[t] < w.hi[t]) w.begin = min(w.begin, w.lo[t]), w.end = max(w.end, w.hi[t]);
@@ -333,17 +334,20 @@ __device__ __forceinline__ void store_k(uint32_t tile, int row0, int lane, const
       for (int i = 0; i < 4; ++i) put8(tile_addr(tile, row, chunk + i), w[i], i < 2 ? s0 : s1);
     }
 }
-// left: keys of each group that exist (the scales of the others may be anything)
+// [from, left): rows of the two groups that some query sees (the scales of the others may be anything)
 template <int D, bool MX>
-__device__ __forceinline__ void store_v(uint32_t tile, int row0, int lane, int left, const Codes<D, MX> &c) {
+__device__ __forceinline__ void store_v(uint32_t tile, int row0, int lane, int from, int left, const Codes<D, MX> &c) {
   const int run = lane >> 2, t = lane & 3;
+  const bool cut = from > 0 || left < 32;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     uint32_t s = c.s[g][0];
-    if (left < 16 * (g + 1)) {
+    if (cut) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (16 * g + 8 * (q >> 1) + 2 * t + (q & 1) >= left) s &= ~(0xFFu << (8 * q));
+      for (int q = 0; q < 4; ++q) {
+        const int row = 16 * g + 8 * (q >> 1) + 2 * t + (q & 1);
+        if (row < from || row >= left) s &= ~(0xFFu << (8 * q));
+      }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -853,7 +857,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar(b), parity, limit, &abort_flag));
     };
     for (int seg = 0; ok && get_work(bars, ring, seg, limit, &abort_flag); ++seg) {
-      const int begin = ring[seg & 1].r.begin, end = ring[seg & 1].r.end, kv_len = ring[seg & 1].r.kv_len, kh = ring[seg & 1].kh;
+      const int begin = ring[seg & 1].r.begin, end = ring[seg & 1].r.end, kv_len = ring[seg & 1].r.kv_len, first_key = ring[seg & 1].r.first_key,
+                kh = ring[seg & 1].kh;
       const int *table = p.b.page_table + (size_t)ring[seg & 1].seq * p.b.max_pages;
       done_work(bars, seg);
       auto page_of = [&](int i, int g) -> int {  // page id of the warp's group g of step i; -1: no keys there
@@ -891,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
         if (i < begin) continue;
         const int nv = n + i - begin, st = nv & 1;
         if (nv >= 2 && !(ok = wait(bars.v_empty[st], ((nv >> 1) - 1) & 1))) break;
-        store_v<D, MX>(base + M::kV + st * M::kTile, 32 * dw, lane, kv_len - (i * kKeys + 32 * dw), cv);
+        store_v<D, MX>(base + M::kV + st * M::kTile, 32 * dw, lane, first_key - (i * kKeys + 32 * dw), kv_len - (i * kKeys + 32 * dw), cv);
         fence_proxy_async();
         mbar_arrive_warp(bar(bars.v_full[st]));
         load_v<D, MX>(v_grp, lane, cv);
