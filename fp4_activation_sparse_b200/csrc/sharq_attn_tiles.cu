@@ -903,97 +903,98 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       }
       n += end - begin;
     }
-  } else if (warp < 14) {
-    // ------------------------------------------------------------------ MMA issue
-    // One warp per row tile: a single one, waiting for one tile's operands and then the other's, left
-    // the tensor pipe idle a third of the time. The whole warp takes every step, so that the elected
-    // thread's operands stay uniform.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    constexpr uint32_t id_s = idesc_f16(kKeys / 2, false), id_o = idesc_f16(D, true);
-    const int t = warp - 12;
-    const bool lead = elect_one();
-    bool ok = true;
-    auto wait = [&](const uint64_t &b, uint32_t parity) {
-      ok = ok && mbar_wait_warp(bar(b), parity, limit, &abort_flag);
-      tc_fence_after();
-    };
-    const uint32_t qd = desc_low(16, base + M::kQ + t * M::kTile), o_tm = tmem + 256 + t * 128, s_tm = tmem + t * 128;
-    const int skip = TWIN ? 1 : 0;  // every second step is the other tile's
-    uint32_t q_n = 0, p_n = 0, items = 0;  // parities of the queries and of the products; there was an item
-    int n0 = 0;                            // key steps of all segments
-    for (int seg = 0; ok && get_work(bars, ring, seg, limit, &abort_flag); ++seg) {
-      const Range &r = ring[seg & 1].r;
-      auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-      const int begin = uniform(r.begin), end = uniform(r.end), lo = uniform(t ? r.lo[1] : r.lo[0]), hi = uniform(t ? r.hi[1] : r.hi[0]);
-      done_work(bars, seg);
-      for (int i = begin - 1; ok && i < end; ++i) {
-        const int n = n0 + i - begin;
-        const bool more = i + 1 < end, products = i >= lo && i < hi && !((i ^ t) & skip),
-                   scores = i + 1 >= lo && i + 1 < hi && !((i + 1 ^ t) & skip);
-        // a tile without keys here waits too: both warps hand every operand tile back, once a step
-        if (more) wait(bars.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
-        if (i >= begin) wait(bars.v_full[n & 1], (n >> 1) & 1);
-        const uint32_t vd = desc_low(16384, base + M::kV + (n & 1) * M::kTile);
-        const uint32_t kd = desc_low(16, base + M::kK + ((n + 1) & 1) * M::kTile);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (products) {
-            // O is written anew with the first product: the segment before must have read it
-            if (h == 0 && i == lo && items) wait(bars.o_empty[t], q_n);
-            wait(bars.p_full[t][h], p_n);
-            if (ok && lead) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ts(o_tm, s_tm + 64 * h + 8 * k, vd + h * 512 + k * 128, id_o, k > 0 || h > 0 || i > lo);
-              tc_commit(bar(bars.pv_done[t][h]));
-            }
-            __syncwarp();
-          }
-          if (scores) {
-            if (h == 0 && i + 1 == lo) {
-              wait(bars.q_full[t], q_n);
-              q_n ^= 1;
-            }
-            if (ok && lead) {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = ((k >> 2) * M::kSlab + (k & 3) * 32) >> 4;
-                mma_ss(s_tm + 64 * h, qd + off, kd + h * 512 + off, id_s, k > 0);
-              }
-              tc_commit(bar(bars.s_full[t][h]));
-            }
-            __syncwarp();
-          }
-        }
-        if (products) p_n ^= 1, items |= i == hi - 1;
-        if (lead) {
-          if (i >= begin) tc_commit(bar(bars.v_empty[n & 1]));
-          if (more) tc_commit(bar(bars.k_empty[(n + 1) & 1]));
-        }
-        __syncwarp();
-      }
-      n0 += end - begin;
-    }
-    // everything issued has finished before tensor memory and shared memory go
-    if (lead) {
-      tc_commit(bar(bars.drain[t]));
-      volatile uint32_t never = 0;
-      mbar_wait(bar(bars.drain[t]), 0, kKvDrainLimitNs, &never);
-    }
-    __syncwarp();
   } else {
-    // ------------------------------------------------------------------ work list
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 14 && lane == 0) {
-      for (int seg = 0;; ++seg) {
-        if (seg >= 2 && !mbar_wait(bar(bars.work_empty[seg & 1]), ((seg >> 1) - 1) & 1, limit, &abort_flag)) break;
-        next_segment<TWIN>(p, row_tiles, share, ring[seg & 1]);
-        const bool end = ring[seg & 1].r.rows <= 0;
-        mbar_arrive(bar(bars.work_full[seg & 1]));
-        if (end) break;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");  // all four warps of the group at one instruction
+    if (warp < 14) {
+      // ------------------------------------------------------------------ MMA issue
+      // One warp per row tile: a single one, waiting for one tile's operands and then the other's, left
+      // the tensor pipe idle a third of the time. The whole warp takes every step, so that the elected
+      // thread's operands stay uniform.
+      constexpr uint32_t id_s = idesc_f16(kKeys / 2, false), id_o = idesc_f16(D, true);
+      const int t = warp - 12;
+      const bool lead = elect_one();
+      bool ok = true;
+      auto wait = [&](const uint64_t &b, uint32_t parity) {
+        ok = ok && mbar_wait_warp(bar(b), parity, limit, &abort_flag);
+        tc_fence_after();
+      };
+      const uint32_t qd = desc_low(16, base + M::kQ + t * M::kTile), o_tm = tmem + 256 + t * 128, s_tm = tmem + t * 128;
+      const int skip = TWIN ? 1 : 0;  // every second step is the other tile's
+      uint32_t q_n = 0, p_n = 0, items = 0;  // parities of the queries and of the products; there was an item
+      int n0 = 0;                            // key steps of all segments
+      for (int seg = 0; ok && get_work(bars, ring, seg, limit, &abort_flag); ++seg) {
+        const Range &r = ring[seg & 1].r;
+        auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+        const int begin = uniform(r.begin), end = uniform(r.end), lo = uniform(t ? r.lo[1] : r.lo[0]), hi = uniform(t ? r.hi[1] : r.hi[0]);
+        done_work(bars, seg);
+        for (int i = begin - 1; ok && i < end; ++i) {
+          const int n = n0 + i - begin;
+          const bool more = i + 1 < end, products = i >= lo && i < hi && !((i ^ t) & skip),
+                     scores = i + 1 >= lo && i + 1 < hi && !((i + 1 ^ t) & skip);
+          // a tile without keys here waits too: both warps hand every operand tile back, once a step
+          if (more) wait(bars.k_full[(n + 1) & 1], ((n + 1) >> 1) & 1);
+          if (i >= begin) wait(bars.v_full[n & 1], (n >> 1) & 1);
+          const uint32_t vd = desc_low(16384, base + M::kV + (n & 1) * M::kTile);
+          const uint32_t kd = desc_low(16, base + M::kK + ((n + 1) & 1) * M::kTile);
+  #pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (products) {
+              // O is written anew with the first product: the segment before must have read it
+              if (h == 0 && i == lo && items) wait(bars.o_empty[t], q_n);
+              wait(bars.p_full[t][h], p_n);
+              if (ok && lead) {
+  #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ts(o_tm, s_tm + 64 * h + 8 * k, vd + h * 512 + k * 128, id_o, k > 0 || h > 0 || i > lo);
+                tc_commit(bar(bars.pv_done[t][h]));
+              }
+              __syncwarp();
+            }
+            if (scores) {
+              if (h == 0 && i + 1 == lo) {
+                wait(bars.q_full[t], q_n);
+                q_n ^= 1;
+              }
+              if (ok && lead) {
+  #pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const uint32_t off = ((k >> 2) * M::kSlab + (k & 3) * 32) >> 4;
+                  mma_ss(s_tm + 64 * h, qd + off, kd + h * 512 + off, id_s, k > 0);
+                }
+                tc_commit(bar(bars.s_full[t][h]));
+              }
+              __syncwarp();
+            }
+          }
+          if (products) p_n ^= 1, items |= i == hi - 1;
+          if (lead) {
+            if (i >= begin) tc_commit(bar(bars.v_empty[n & 1]));
+            if (more) tc_commit(bar(bars.k_empty[(n + 1) & 1]));
+          }
+          __syncwarp();
+        }
+        n0 += end - begin;
       }
+      // everything issued has finished before tensor memory and shared memory go
+      if (lead) {
+        tc_commit(bar(bars.drain[t]));
+        volatile uint32_t never = 0;
+        mbar_wait(bar(bars.drain[t]), 0, kKvDrainLimitNs, &never);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ work list
+      if (warp == 14 && lane == 0) {
+        for (int seg = 0;; ++seg) {
+          if (seg >= 2 && !mbar_wait(bar(bars.work_empty[seg & 1]), ((seg >> 1) - 1) & 1, limit, &abort_flag)) break;
+          next_segment<TWIN>(p, row_tiles, share, ring[seg & 1]);
+          const bool end = ring[seg & 1].r.rows <= 0;
+          mbar_arrive(bar(bars.work_full[seg & 1]));
+          if (end) break;
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
   __syncthreads();
   if (warp == 12) {
