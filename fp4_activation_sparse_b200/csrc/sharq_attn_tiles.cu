@@ -233,6 +233,39 @@ struct Work {
   ItemParts parts;
 };
 
+// Entries: the row tiles of sequence after sequence. Every sequence has as many places as the longest may need
+// where one chunk of the block's threads holds them all. Else sequence b begins at b plus the whole row
+// tiles of the rows before it: two places too many at most, so that one long prompt among many single
+// tokens, or a loose bound on the rows, costs nothing.
+struct Entries {
+  int row_tiles;  // of the longest sequence
+  bool dense;
+  __device__ __forceinline__ Entries(const AttnParams &p, int rt)
+      : row_tiles(rt), dense(rt == 1 || (long long)p.b.n_seq * rt <= kThreads) {}
+  __device__ __forceinline__ static long long rows_before(const AttnParams &p, int seq) {
+    return (long long)min(max(__ldg(p.b.cu_q + seq), 0), p.b.tokens) * p.group;
+  }
+  __device__ __forceinline__ int first(const AttnParams &p, int seq) const {
+    return seq + (int)(rows_before(p, seq) / (2 * kRows) - rows_before(p, 0) / (2 * kRows));
+  }
+  __device__ __forceinline__ long long count(const AttnParams &p) const {
+    return dense ? (long long)p.b.n_seq * row_tiles : first(p, p.b.n_seq);
+  }
+  __device__ __forceinline__ void find(const AttnParams &p, int entry, int &seq, int &rt) const {
+    if (dense) {
+      seq = entry / row_tiles, rt = entry - seq * row_tiles;
+      return;
+    }
+    int lo = 0, hi = p.b.n_seq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first(p, mid) <= entry) lo = mid;
+      else hi = mid - 1;
+    }
+    seq = lo, rt = entry - first(p, lo);
+  }
+};
+
 template <bool TWIN>
 __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt) {
   Range w;
@@ -383,40 +416,57 @@ __device__ __forceinline__ void st256(void *p, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), SHARQ_I8(v, 0) : "memory");
 }
 
-// The share's next segment (rows 0: none is left). One thread; the walk's state stays in `sh`.
+// The work list's warp: where its walk over the share stands, the same in every lane.
+struct Walk {
+  long long at, end, first;  // the share's next unit of cost and its end; where the costs of (seq, rt) begin
+  int seq, rt;
+};
+
+// The share's next segment to `out` (rows 0: none is left).
 template <bool TWIN>
-__device__ __forceinline__ void next_segment(const AttnParams &p, int row_tiles, Share &sh, Work &out) {
-  const int heads = p.c.kv_heads;
-  const long long at = sh.cut[0];
-  out.r.rows = 0;
-  if (at >= sh.cut[1]) return;
+__device__ __forceinline__ void next_segment(const AttnParams &p, const Share &sh, Walk &walk, Work &out) {
+  const int heads = p.c.kv_heads, lane = threadIdx.x & 31;
   Work x;
-  int cost;
-  long long first = sh.first;
-  for (;; ++sh.entry) {  // entries without rows have no steps
-    x.seq = sh.entry / row_tiles;
-    x.r = item_range<TWIN>(p, x.seq, sh.entry % row_tiles);
+  int cost = 0;
+  x.r.rows = 0;
+  while (walk.at < walk.end && walk.seq < p.b.n_seq) {
+    x.seq = walk.seq;
+    x.r = item_range<TWIN>(p, walk.seq, walk.rt);
     cost = x.r.cost();
-    if (at < first + (long long)cost * heads) break;
-    first += (long long)cost * heads;
-  }
-  sh.first = first;
-  x.kh = small_quotient(at - first, cost);
-  const long long p0 = first + (long long)x.kh * cost, p1 = p0 + cost;
-  const long long to = min(sh.cut[1], p1);
-  x.parts = item_parts<kItemCost>(sh, p0, p1, at);
-  if (x.r.begin < x.r.end) {
-    const int from = at == p0 ? x.r.begin : x.r.begin + (int)(at - p0) - kItemCost;
-    const int until = x.r.begin + (int)(to - p0) - kItemCost;
-    x.r.begin = from, x.r.end = until;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      x.r.lo[t] = max(x.r.lo[t], from), x.r.hi[t] = min(x.r.hi[t], until);
-      if (TWIN) x.r.lo[t] += (x.r.lo[t] ^ t) & 1, x.r.hi[t] -= ((x.r.hi[t] - 1) ^ t) & 1;
+    if (walk.at < walk.first + (long long)cost * heads) break;
+    walk.first += (long long)cost * heads;
+    const int rows = x.r.rows;
+    x.r.rows = 0;
+    ++walk.rt;
+    if (rows == 2 * kRows) continue;
+    // the next sequence with new tokens, 32 at a time
+    walk.rt = 0;
+    uint32_t some = 0;
+    for (++walk.seq; walk.seq < p.b.n_seq; walk.seq += 32) {
+      const int i = walk.seq + lane;
+      some = __ballot_sync(0xFFFFFFFFu, i < p.b.n_seq && __ldg(p.b.cu_q + i + 1) > __ldg(p.b.cu_q + i));
+      if (some) break;
     }
+    if (some) walk.seq += __ffs(some) - 1;
   }
-  sh.cut[0] = to;
-  out = x;
+  if (x.r.rows > 0) {
+    x.kh = small_quotient(walk.at - walk.first, cost);
+    const long long p0 = walk.first + (long long)x.kh * cost, p1 = p0 + cost;
+    const long long to = min(walk.end, p1);
+    x.parts = item_parts<kItemCost>(sh, p0, p1, walk.at);
+    if (x.r.begin < x.r.end) {
+      const int from = walk.at == p0 ? x.r.begin : x.r.begin + (int)(walk.at - p0) - kItemCost;
+      const int until = x.r.begin + (int)(to - p0) - kItemCost;
+      x.r.begin = from, x.r.end = until;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        x.r.lo[t] = max(x.r.lo[t], from), x.r.hi[t] = min(x.r.hi[t], until);
+        if (TWIN) x.r.lo[t] += (x.r.lo[t] ^ t) & 1, x.r.hi[t] -= ((x.r.hi[t] - 1) ^ t) & 1;
+      }
+    }
+    walk.at = to;
+  }
+  if (lane == 0) out = x;
 }
 
 // A warp's 32 query rows of a segment to the shared-memory tile, D/16 lanes (32 bytes each) per row,
@@ -507,8 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
     kv_mbar_init(bar(bars.twin_empty), 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  find_share<kThreads, kItemCost>((long long)p.b.n_seq * row_tiles, p.c.kv_heads, kItemCost + 2, &share, warp_sums,
-                                  [&](long long e) { return item_range<TWIN>(p, (int)e / row_tiles, (int)e % row_tiles).cost(); });
+  const Entries entries(p, row_tiles);
+  find_share<kThreads, kItemCost>(entries.count(p), p.c.kv_heads, kItemCost + 2, &share, warp_sums, [&](long long e) {
+    int seq, rt;
+    entries.find(p, (int)e, seq, rt);
+    return rt < row_tiles ? item_range<TWIN>(p, seq, rt).cost() : 0;
+  });
   if (share.cut[0] >= share.cut[1]) return;
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(kv_smem_u32(&tmem_slot)), "r"(kTmemCols));
@@ -984,12 +1038,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
       __syncwarp();
     } else {
       // ------------------------------------------------------------------ work list
-      if (warp == 14 && lane == 0) {
+      if (warp == 14) {
+        Walk walk{share.cut[0], share.cut[1], share.first, 0, 0};
+        entries.find(p, share.entry, walk.seq, walk.rt);
         for (int seg = 0;; ++seg) {
-          if (seg >= 2 && !mbar_wait(bar(bars.work_empty[seg & 1]), ((seg >> 1) - 1) & 1, limit, &abort_flag)) break;
-          next_segment<TWIN>(p, row_tiles, share, ring[seg & 1]);
+          if (seg >= 2 && !mbar_wait_warp(bar(bars.work_empty[seg & 1]), ((seg >> 1) - 1) & 1, limit, &abort_flag)) break;
+          next_segment<TWIN>(p, share, walk, ring[seg & 1]);
+          __syncwarp();
           const bool end = ring[seg & 1].r.rows <= 0;
-          mbar_arrive(bar(bars.work_full[seg & 1]));
+          mbar_arrive_warp(bar(bars.work_full[seg & 1]));
           if (end) break;
         }
       }
@@ -1010,7 +1067,6 @@ int row_tiles(const AttnParams &p) {
 template <int D, bool MX, bool TWIN>
 cudaError_t launch_t(const AttnParams &p, cudaStream_t st) {
   auto kernel = attn_tiles_kernel<D, MX, TWIN>;
-  if ((long long)p.b.n_seq * row_tiles(p) > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   static SmemOnce once;
   if (cudaError_t e = once.set(kernel, TileSmem<D>::kTotal)) return e;
   kernel<<<sm_count(), kThreads, TileSmem<D>::kTotal, st>>>(p, row_tiles(p));
