@@ -436,11 +436,25 @@ def _address(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+def _stream_handle(stream, device: torch.device) -> int:
+    """The raw handle of a stream: an object with `cuda_stream` (of the call's device, where it says) or an integer."""
+    own = getattr(stream, "device", None)
+    if own is not None and torch.device(own) != device:
+        _reject(f"the stream is of {own}, the call on {device}")
+    try:
+        return int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+    except (TypeError, ValueError):
+        _reject(f"stream must be a stream or its handle (got {type(stream).__name__})")
+
+
 def _on_stream(stream, device: torch.device):
-    """`stream` (a Stream or a raw handle) as the current one: what a call allocates and clears, and
-    what it launches, is then ordered on it."""
+    """`stream` as the current one: what a call allocates and clears, and what it launches, is then
+    ordered on it. Handles 0 and 1 are the device's default stream."""
+    handle = _stream_handle(stream, device)
+    if device.type != "cuda":
+        _reject(f"the call is on {device}, not on a CUDA device")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device=device)
     return torch.cuda.stream(stream)
 
 
