@@ -332,7 +332,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       // ---- masks
       const bool whole = valid == 3u && key0 + kTile <= kv_len &&
                          (!p.causal || (key0 + kTile - 1 <= pos_lo && (p.window <= 0 || pos_hi - key0 < p.window)));
+      uint32_t keep[2] = {~0u, ~0u};  // the lane's value scales of keys that some query sees
       if (!whole) {
+        // the others may be anything: zero keeps 0 * v from NaN
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = key0 + 16 * h + 8 * (q >> 1) + 2 * t + (q & 1);
+            if (key < first_key || key >= kv_len) keep[h] &= ~(0xFFu << (8 * q));
+          }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -422,15 +431,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
         lds128(vc + lane * 16, v[0]);
         if (D == 128) lds128(vc + 512 + lane * 16, v[1]);
         constexpr int per_run = (MX ? 32 : 16) / (D / 8);  // runs that share a block: 1, 2 or 4
-        uint32_t vs = lds32(st + h * G.bytes + G.v_scales + (g / per_run * 4 + t) * 4);
-        if (!whole) {  // scales of keys that no query sees may be anything: zero keeps 0 * v from NaN
-          const int from = first_key - (key0 + 16 * h), left = kv_len - (key0 + 16 * h);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int key = 8 * (q >> 1) + 2 * t + (q & 1);
-            if (key < from || key >= left) vs &= ~(0xFFu << (8 * q));
-          }
-        }
+        const uint32_t vs = lds32(st + h * G.bytes + G.v_scales + (g / per_run * 4 + t) * 4) & keep[h];
         const uint32_t s0 = kv_scales2<MX>(vs & 0xFFFFu), s1 = kv_scales2<MX>(vs >> 16);
         uint32_t even[2][2], odd[2][2];  // [word][slot half]: nibbles of two keys of one element per byte
 #pragma unroll
