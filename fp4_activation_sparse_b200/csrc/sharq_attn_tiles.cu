@@ -3,7 +3,7 @@
 // One block works on 256 query rows of one key head (the group's heads of consecutive tokens: row
 // i * group + g) as two 128-row tiles, and walks the keys in tiles of 128. Both contractions run on
 // the tensor cores from float16 operands with float32 accumulators in tensor memory:
-//   S_t = Q_t K^T   Q_t and K in shared memory; Q scaled by a power of two per row (exact)
+//   S_t = Q_t K^T   Q_t and K in shared memory; Q scaled by a power of two per row
 //   O_t += P_t V    P_t in tensor memory (over S_t's columns), V in shared memory as stored
 // The cache's codes become float16 on the way into shared memory: code * block scale is exact there
 // (2 + 4 significant bits; the E8M0 exponents of the cache are limited to float16's range). The
@@ -233,6 +233,9 @@ struct Work {
   ItemParts parts;
 };
 
+// A boundary of cu_q as one of the call's rows, so that rows and entries stay what they are for each other.
+__device__ __forceinline__ int token_row(const AttnParams &p, int at) { return min(max(at, 0), p.b.tokens); }
+
 // Entries: the row tiles of sequence after sequence. Every sequence has as many places as the longest may need
 // where one chunk of the block's threads holds them all. Else sequence b begins at b plus the whole row
 // tiles of the rows before it: two places too many at most, so that one long prompt among many single
@@ -243,7 +246,7 @@ struct Entries {
   __device__ __forceinline__ Entries(const AttnParams &p, int rt)
       : row_tiles(rt), dense(rt == 1 || (long long)p.b.n_seq * rt <= kThreads) {}
   __device__ __forceinline__ static long long rows_before(const AttnParams &p, int seq) {
-    return (long long)min(max(__ldg(p.b.cu_q + seq), 0), p.b.tokens) * p.group;
+    return (long long)token_row(p, __ldg(p.b.cu_q + seq)) * p.group;
   }
   __device__ __forceinline__ int first(const AttnParams &p, int seq) const {
     return seq + (int)(rows_before(p, seq) / (2 * kRows) - rows_before(p, 0) / (2 * kRows));
@@ -273,7 +276,7 @@ __device__ __forceinline__ Range item_range(const AttnParams &p, int seq, int rt
   w.q0 = __ldg(p.b.cu_q + seq);
   w.kv_len = __ldg(p.b.kv_len + seq);
   w.row0 = rt * 2 * kRows;
-  w.rows = min(min(q1 - w.q0, p.b.max_q) * p.group - w.row0, 2 * kRows);
+  w.rows = min(min(token_row(p, q1) - token_row(p, w.q0), p.b.max_q) * p.group - w.row0, 2 * kRows);
   w.first_pos = w.kv_len - (q1 - w.q0);
   const int reach = min(w.kv_len, p.b.max_pages << p.c.page_shift);  // no place behind the table
   w.begin = 0x7FFFFFFF, w.end = 0;
@@ -470,8 +473,9 @@ __device__ __forceinline__ void next_segment(const AttnParams &p, const Share &s
 }
 
 // A warp's 32 query rows of a segment to the shared-memory tile, D/16 lanes (32 bytes each) per row,
-// all loads in flight at once. The row's largest value moves to [2^12, 2^13): exact in float16 down
-// to 2^-36 of it. The sign of the score's factor goes into the query, so that maxima stay maxima.
+// all loads in flight at once. The row's largest value moves to [2^12, 2^13): eight significant bits
+// are exact in float16 from 2^-17 on, 2^-29 of the largest, and an element below that is rounded by at most
+// 2^-25, 2^-37 of the largest. The sign of the score's factor goes into the query, so that maxima stay maxima.
 template <int D, bool MX>
 __device__ __forceinline__ void load_queries(const AttnParams &p, const Work &w, int first, int row_base, int lane, uint32_t q_tile,
                                              float *coef) {

@@ -80,3 +80,30 @@ def test_more_sequences_times_row_tiles_than_an_index_holds():
         k, v = small.kv(b, c)
         check_attention(y[at:at + m], lse[at:at + m], K.attention(x[at:at + m], k, v, c - m, True, 0, 0.125), f"sequence {b}")
         at += m
+
+
+@pytest.mark.parametrize("count,first", [(3, 100), (300, 700)])
+def test_index_arrays_that_run_past_the_tensors(count, first):
+    """Rows behind the call's tensors are left out, the others and the workspace stay right."""
+    S = require_gpu()
+    rng = np.random.default_rng(count)
+    new = [first] + [60] * 2 + [1] * (count - 3)
+    lengths = [n + 20 for n in new]
+    st = Setup(S, rng, lengths, 1, 64, "nvfp4", 32).fill()
+    tokens = first + 90
+    q, x = bf16(rng, tokens, 4, 64)
+    cut, full = st.batch(new, tokens=tokens), st.batch(new)
+    ws = S.alloc_attention_workspace(st.cache, full, 4)
+    y, lse = S.sharq_attention(q, st.cache, cut, return_lse=True, workspace=ws)
+    for b, rows in ((0, first), (1, 60), (2, 30)):
+        at = sum(new[:b])
+        k, v = st.kv(b, lengths[b])
+        check_attention(y[at:at + rows], lse[at:at + rows], K.attention(x[at:at + rows], k, v, 20, True, 0, 0.125), f"sequence {b}")
+    all_q = torch.zeros(sum(new), 4, 64, dtype=torch.bfloat16, device="cuda")
+    all_q[:tokens] = q
+    y2, lse2 = S.sharq_attention(all_q, st.cache, full, return_lse=True, workspace=ws)
+    for b in range(count):
+        at = sum(new[:b])
+        k, v = st.kv(b, lengths[b])
+        rows = slice(at, at + new[b])
+        check_attention(y2[rows], lse2[rows], K.attention(all_q[rows].double().cpu().numpy(), k, v, 20, True, 0, 0.125), f"sequence {b}")
