@@ -5,8 +5,8 @@
 // 16-row side of the matrix instruction holds keys and value elements and the 8-column side the
 // few query rows. Codes become float16 in registers: code * block scale is exact there (2 + 4
 // significant bits; the cache's E8M0 exponents are limited to float16's range), the second-level
-// scales and the softmax scale are applied in float32. Queries are scaled by a power of two per
-// row and are exact in float16 too. Probabilities are rounded to float16 (11 bits, against the
+// scales and the softmax scale are applied in float32. Queries are scaled by a power of two per row and
+// are exact in float16 down to 2^-29 of the row's largest. Probabilities are rounded to float16 (11 bits, against the
 // 8 of the bfloat16 output); their sum, the maxima and both accumulators are float32.
 //
 // Bound by the cache's bytes (144 or 136 per key and key head at 128 elements). Every block takes an
@@ -253,8 +253,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) attn_rows_kernel
       for (int i = 0; i < KS * 2; ++i) am = max3abs(am, bf16lo(raw[i]), bf16hi(raw[i]));
       am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
       am = fmaxf(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-      // the row's largest value moves to [2^12, 2^13): exact in float16 down to 2^-36 of it; the sign of
-      // the score's factor goes into the query, so that maxima stay maxima
+      // the row's largest value moves to [2^12, 2^13). Float16's last step there is 2^-24, so that eight
+      // significant bits are exact from 2^-17 on, 2^-29 of the largest; below that an element is rounded, by
+      // at most 2^-25: 2^-37 of the largest. The sign of the score's factor goes into the query, so that
+      // maxima stay maxima
       const int e = max((int)(__float_as_uint(am) >> 23) - 127, -100);
       const float up = copysignf(__uint_as_float((uint32_t)(127 + 12 - e) << 23), factor);
 #pragma unroll

@@ -377,7 +377,8 @@ int sharq_kv_read(const sharq_kv_cache *cache, const sharq_kv_batch *batch, void
  * If a bounded device wait gives up, the call's outputs are undefined, sharq_device_status reports
  * SHARQ_ERR_TIMEOUT, and the workspace must be zeroed again before it is reused.
  * A query that sees nothing gives y = 0 and lse = -inf. Scores, maxima, sums and outputs are
- * float32; probabilities enter the value product as float16 relative to a running maximum. */
+ * float32; probabilities enter the value product as float16 relative to a running maximum; a query's
+ * elements are exact down to 2^-29 of its row's largest, below that rounded by at most 2^-37 of it. */
 size_t sharq_attention_workspace_size(const sharq_kv_cache *cache, const sharq_kv_batch *batch, int q_heads);
 int sharq_attention(const void *q_bf16_dev, long long q_stride, int q_heads, const sharq_kv_cache *cache,
                     const sharq_kv_batch *batch, int causal, int window, float scale, void *y_dev, float *lse_dev,
