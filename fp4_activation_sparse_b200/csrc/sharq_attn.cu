@@ -15,11 +15,12 @@
 // segment's 32-key tiles in turn, each with copies of its own in flight, and join at its end. The
 // parts of an item that is cut between blocks go through the workspace; the block that arrives last
 // joins them in the order of the keys. Bulk copies (one per group of 16 tokens, issued by the lane that
-// looked up its page) keep the copying out of the instruction stream, which is the bound in
-// fact: about 640 instructions per 32 keys and warp, half of them turning codes into float16.
+// looked up its page) keep the copying out of the instruction stream: about 640 instructions per 32 keys and
+// warp, half of them turning codes into float16. No unit is full (issue 0.6 per cycle, the busiest pipe half the
+// time): with 3.8 warps per scheduler their latencies are not hidden.
 //
-// Measured (32 query and 8 key heads of 128): 64 contexts of 33 to 8191 tokens 73 us, 4.2 TB/s; two of
-// 120 to 131 thousand 65 us, 4.2 TB/s; one of 777 tokens 9 us, which is latency. Tried without gain: more
+// Measured (32 query and 8 key heads of 128): 64 contexts of 33 to 8191 tokens 74 us, 4.2 TB/s; two of
+// 120 to 131 thousand 66 us, 4.1 TB/s; one of 777 tokens 9 us, which is latency. Tried without gain: more
 // warps (ten or twelve of them spill: 90 and 116 us for the 64 contexts), a third tile in the ring,
 // the score products split into two chains.
 #include "sharq_common.cuh"
@@ -625,10 +626,11 @@ cudaError_t launch_d(const AttnParams &p, cudaStream_t st) {
 }  // namespace
 
 namespace {
-// 32 rows: what one block of the kernel above holds in registers. With 7 and 4 rows per token it takes, for
-// 16 contexts, 22, 34, 35 us at 14, 21, 28 rows where the 128-row tiles take 38, 38, 37, and 36, 60, 62 at
-// 16, 24, 32 rows where they take 65; for one context of 50000 tokens and one key head 18, 25, 29 at
-// 12, 24, 32 rows.
+// Up to 16 rows the kernel above holds everything in registers; its form for 17 to 32 spills at 128 elements
+// (372 bytes of stores) and pads to 32. For 16 contexts of 1500 to 6000 tokens it takes 22, 35, 37 us at 14,
+// 21, 28 rows (4 key heads) where the 128-row tiles take 40, and 34, 57, 60 us at 16, 24, 32 rows (8 key
+// heads) where they take 58; for one context of 50000 tokens and one key head 17, 25, 28 us at 12, 24, 32
+// rows where they take 45 to 49.
 bool use_tiles(const AttnParams &p) { return (long long)p.b.max_q * p.group > 32; }
 }  // namespace
 

@@ -44,10 +44,10 @@
 // splits of the registers, the halves unrolled, scores and probabilities in places of their own (the
 // wait that this removes is covered by the other tile: 2 % slower).
 //
-// Measured (NVFP4): one prompt of 8192 tokens, 32 query and 8 key heads of 128, 535 to 560 us with the
-// board's power, 980 to 1025 TFLOP/s; 9360 queries over 512 cached keys, 40 heads, 164 to 172 us; pieces of
-// four prompts in a window of 4096 (64 elements, MXFP4) 87 us; 3 to 5 drafted tokens of 16 contexts, 28
-// query and 4 key heads, 40 us.
+// Measured (NVFP4): one prompt of 8192 tokens, 32 query and 8 key heads of 128, 540 to 560 us with the
+// board's power, 980 to 1015 TFLOP/s; 9360 queries over 512 cached keys, 40 heads, 167 us; pieces of four
+// prompts in a window of 4096 (64 elements, MXFP4) 89 us; 3 to 5 drafted tokens of 16 contexts, 28 query
+// and 4 key heads, 42 us; 256 single tokens beside a prompt of 8192, 741 us.
 //
 // Every mbarrier wait is bounded; on expiry the block records a status word, stops issuing, waits
 // for what it issued, frees its tensor memory and exits.

@@ -319,6 +319,8 @@ typedef struct {
  * row x % page_size. A position past the table, or whose page id is negative or >= num_pages, has
  * no place: appends to it are dropped, reads give zeros, attention does not see it. Rows at or
  * behind cu_q[n_seq] (padding) belong to no sequence and are left as they were in every output.
+ * What stands at places that a call does not look at (positions from kv_len on, positions ahead of
+ * every window) may be anything, never written bytes included.
  * The index arrays are device memory, read when the kernels run (a captured call follows them). */
 typedef struct {
   const int *cu_q;       /* [n_seq + 1], increasing (equal: a sequence without new tokens) */
@@ -357,7 +359,8 @@ int sharq_kv_append(const void *qkv_bf16_dev, long long row_stride, int q_heads,
 
 /* Read the batch's token rows back as the values they stand for (one launch): prefix export,
  * checks, calibration of the second-level scales.
- *   k_out_dev, v_out_dev  [tokens][kv_heads][head_dim], bf16 (rounded once) or float32 */
+ *   k_out_dev, v_out_dev  [tokens][kv_heads][head_dim], float32 (code * block scale is exact, times the
+ *                 second-level scale), or that rounded to bf16 */
 int sharq_kv_read(const sharq_kv_cache *cache, const sharq_kv_batch *batch, void *k_out_dev, void *v_out_dev,
                   int out_dtype, void *stream);
 
@@ -419,8 +422,8 @@ int sharq_mma_peak(int mode, int fmt, int iters, int clusters, void *stream);
  * bounded waits set when they give up: SHARQ_OK or SHARQ_ERR_TIMEOUT (or SHARQ_ERR_CUDA). */
 int sharq_device_status(void *stream);
 
-/* Test hook: time limit, in nanoseconds, of the GEMM's bounded waits and of the per-tensor
- * preparation's grid barrier (0 restores the default of 4 s). Process-wide (one atomic value
+/* Test hook: time limit, in nanoseconds, of the GEMM's and the attention's bounded waits and of the
+ * per-tensor preparation's grid barrier (0 restores the default of 4 s). Process-wide (one atomic value
  * shared by every host thread), read by each call when it launches. Lowering it lets a test make a wait give up without faulting the device:
  * the kernel records SHARQ_ERR_TIMEOUT, drains its own copies and MMAs, frees its tensor
  * memory and returns; its output is then undefined. Applies to calls issued afterwards. */
