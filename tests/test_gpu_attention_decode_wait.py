@@ -1,5 +1,7 @@
 """The decode kernel's bounded wait reports that it gave up, and the next call is right. It waits for a
-warp's copies of 32 keys, issued at most one such tile before: from DRAM they are not there at once."""
+warp's copies of 32 keys, issued at most one such tile before: from DRAM they are not there at once. (Up to
+16 query rows, 40 of 40 calls whose cache had left the L2 reported it; the 17-row form works so long on a
+tile that only some do, so that it is no case here.)"""
 import numpy as np
 import pytest
 import torch
@@ -11,7 +13,7 @@ from tests.kv_common import Setup, bf16, check_attention
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("new,group", [(1, 4), (3, 4), (4, 7)])
+@pytest.mark.parametrize("new,group", [(1, 4), (3, 4), (2, 8)])
 def test_timeout_is_reported_and_the_next_call_is_right(new, group):
     S = require_gpu()
     rng = np.random.default_rng(new)
