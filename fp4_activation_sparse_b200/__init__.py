@@ -438,13 +438,15 @@ def _address(t: torch.Tensor | None):
 
 def _stream_handle(stream, device: torch.device) -> int:
     """The raw handle of a stream: an object with `cuda_stream` (of the call's device, where it says) or an integer."""
-    own = getattr(stream, "device", None)
-    if own is not None and torch.device(own) != device:
-        _reject(f"the stream is of {own}, the call on {device}")
     try:
-        return int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
-    except (TypeError, ValueError):
+        own = getattr(stream, "device", None)
+        own = device if own is None else torch.device(own)
+        handle = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+    except (TypeError, ValueError, RuntimeError):
         _reject(f"stream must be a stream or its handle (got {type(stream).__name__})")
+    if own.type != device.type or own.index not in (None, device.index):
+        _reject(f"the stream is of {own}, the call on {device}")
+    return handle
 
 
 def _on_stream(stream, device: torch.device):

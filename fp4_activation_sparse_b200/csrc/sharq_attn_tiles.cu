@@ -994,14 +994,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
           if (i >= begin) wait(bars.v_full[n & 1], (n >> 1) & 1);
           const uint32_t vd = desc_low(16384, base + M::kV + (n & 1) * M::kTile);
           const uint32_t kd = desc_low(16, base + M::kK + ((n + 1) & 1) * M::kTile);
-  #pragma unroll
+#pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (products) {
               // O is written anew with the first product: the segment before must have read it
               if (h == 0 && i == lo && items) wait(bars.o_empty[t], q_n);
               wait(bars.p_full[t][h], p_n);
               if (ok && lead) {
-  #pragma unroll
+#pragma unroll
                 for (int k = 0; k < 4; ++k)
                   mma_ts(o_tm, s_tm + 64 * h + 8 * k, vd + h * 512 + k * 128, id_o, k > 0 || h > 0 || i > lo);
                 tc_commit(bar(bars.pv_done[t][h]));
@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const __grid_co
                 q_n ^= 1;
               }
               if (ok && lead) {
-  #pragma unroll
+#pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                   const uint32_t off = ((k >> 2) * M::kSlab + (k & 3) * 32) >> 4;
                   mma_ss(s_tm + 64 * h, qd + off, kd + h * 512 + off, id_s, k > 0);

@@ -16,12 +16,13 @@ DEVICE = torch.device("cuda", 0)
 
 
 @pytest.mark.parametrize("stream,handle", [(0, 0), (0x5550, 0x5550), (Wrapper(0x40), 0x40), (Wrapper(0x40, "cuda:0"), 0x40),
-                                           (Wrapper(0, DEVICE), 0)])
+                                           (Wrapper(0, DEVICE), 0), (Wrapper(0x40, "cuda"), 0x40), (Wrapper(0x40, 0), 0x40)])
 def test_handles(stream, handle):
     assert S._stream_handle(stream, DEVICE) == handle
 
 
-@pytest.mark.parametrize("stream", [Wrapper(0x40, "cuda:1"), Wrapper(0x40, torch.device("cuda", 3)), Wrapper(None), "main", object()])
+@pytest.mark.parametrize("stream", [Wrapper(0x40, "cuda:1"), Wrapper(0x40, torch.device("cuda", 3)), Wrapper(None), "main", object(),
+                                    Wrapper(0x40, "somewhere"), Wrapper(0x40, "cpu"), Wrapper(0x40, 1)])
 def test_refused(stream):
     """A stream of another device would be dropped in silence; something else is no stream."""
     for call in (S._stream_handle, S._on_stream):
