@@ -659,6 +659,7 @@ int sharq_norm_residual(const void *y, const void *residual, int tokens, int k, 
   p.eps = eps;
   p.tokens = tokens;
   p.k = k;
+  p.inv_k = 1.0 / k;
   p.rows_per_gate = rows_per_gate;
   cudaError_t e = sharq::launch_norm_residual(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "sharq_norm_residual");

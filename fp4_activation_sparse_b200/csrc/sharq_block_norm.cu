@@ -4,11 +4,12 @@
 //   h  = bf16(r' * rstd(r') * pre_gamma)   (optional; rstd of r' as stored)
 // Bound by its bytes: y and r read once, r' and h written once, 8 bytes per element. One block
 // per row keeps the row in registers between the two reductions, so nothing is read twice.
-// Measured: 32760 x 5120 with a gate and both norms 227 us (5.9 TB/s). The squares are added in float64 one
-// by one, as the stand-alone norm does, so that a row's rstd is the same to the bit: 12 us of the 227
-// (with eight squares in float32 first, off by up to 4e-7, it took 215 us); as (x 2^-896)(x 2^896) from
-// four instructions per element instead of the three here it took 233. Loading the next row ahead in a
-// persistent block gained nothing. Few rows take a unit per thread (16 x 4096: 3.2 us, against 5.1 with four).
+// Measured: 32760 x 5120 with a gate and both norms 216 us (6.2 TB/s). The squares are added in float64 one
+// by one, as the stand-alone norm does, so that a row's rstd is the same to the bit: 2 us of the 216 (with eight
+// squares in float32 first, off by up to 4e-7, it took 214). A conversion per element is cheaper than
+// building the double from the bits (226), and the division by k is a product with the host's 1/k (a step of
+// float64 apart; 222 with it in every warp). Loading the next row ahead in a persistent block gained nothing.
+// Few rows take a unit per thread (16 x 4096: 3.1 us, against 5.1 with four).
 #include "sharq_common.cuh"
 #include "sharq_internal.h"
 #include "sharq_kv.h"
@@ -25,25 +26,13 @@ __device__ __forceinline__ uint4 ld128(const void *p) {
 
 // rstd of a row from every thread's sum; every warp adds the warps' sums itself, so one barrier is
 // enough. red: this norm's own.
-__device__ __forceinline__ float block_rstd(double ss, int k, float eps, double *red) {
+__device__ __forceinline__ float block_rstd(double ss, double inv_k, float eps, double *red) {
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
   __syncthreads();
   double t = 0.0;
   for (int i = 0; i < (int)(blockDim.x >> 5); ++i) t += red[i];
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(__double2float_rn(__ddiv_rn(t, (double)k)), eps)));
-}
-
-// A thread's sum from the scaled one; once more with infinities and NaN where it may hold some.
-template <int U>
-__device__ __forceinline__ double unscaled(const uint4 (&v)[U], int units, double ss) {
-  if (ss < 1.0) return ss * 0x1p256;
-  ss = 0.0;
-#pragma unroll
-  for (int i = 0; i < U; ++i)
-    if (threadIdx.x + i * blockDim.x < units)
-      ss = add_squares_exact(v[i].w, add_squares_exact(v[i].z, add_squares_exact(v[i].y, add_squares_exact(v[i].x, ss))));
-  return ss;
+  return __frcp_rn(__fsqrt_rn(__fadd_rn(__double2float_rn(t * inv_k), eps)));
 }
 
 // One row from its y and r in registers, U 16-byte units (8 bf16) per thread.
@@ -58,9 +47,8 @@ __device__ __forceinline__ void norm_row(const NormResidualParams &p, size_t row
   if (p.post_gamma) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (threadIdx.x + i * blockDim.x < units) ss = add_squares_scaled(y[i], ss);
-    ss = unscaled<U>(y, units, ss);
-    rs = block_rstd(ss, p.k, p.eps, red[0]);
+      if (threadIdx.x + i * blockDim.x < units) ss = add_squares(y[i], ss);
+    rs = block_rstd(ss, p.inv_k, p.eps, red[0]);
   }
   ss = 0.0;
 #pragma unroll
@@ -88,13 +76,12 @@ __device__ __forceinline__ void norm_row(const NormResidualParams &p, size_t row
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         rw[j] = *reinterpret_cast<const uint32_t *>(&h);
       }
-      if (p.pre_gamma) ss = add_squares_scaled(r[i], ss);
+      if (p.pre_gamma) ss = add_squares(r[i], ss);
       __stcs(reinterpret_cast<uint4 *>(p.residual_out + row * p.k) + u, r[i]);
     }
   }
   if (!p.pre_gamma) return;
-  ss = unscaled<U>(r, units, ss);
-  rs = block_rstd(ss, p.k, p.eps, red[1]);
+  rs = block_rstd(ss, p.inv_k, p.eps, red[1]);
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int u = threadIdx.x + i * blockDim.x;

@@ -90,6 +90,7 @@ struct NormResidualParams {
   const uint16_t *y, *post_gamma, *gate, *residual, *pre_gamma;
   uint16_t *residual_out, *h_out;
   float alpha, eps;
+  double inv_k;  // 1 / k
   int tokens, k, rows_per_gate;
 };
 

@@ -66,16 +66,12 @@ __device__ __forceinline__ uint32_t kv_scales2(uint32_t two) {
   return d;
 }
 
-// ss + a unit's eight squares * 2^-256, every addition in float64. An element's bits under an exponent field
-// raised by 768 are |x| * 2^-128 in two instructions (a square, 16 bits, is exact); a zero or subnormal
-// comes out below 2^-254 and cannot reach a float32 mean. Infinities and NaN are values of at least 1
-// there, and larger than any other: a sum below 1 has none.
-__device__ __forceinline__ double add_squares_scaled(const uint4 &v, double ss) {
+// ss + a unit's eight squares, exact products and every addition in float64.
+__device__ __forceinline__ double add_squares(const uint4 &v, double ss) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const double a = __hiloint2double((int)((w[i] << 13 & 0x0FFFE000u) | 0x30000000u), 0);
-    const double b = __hiloint2double((int)((w[i] >> 3 & 0x0FFFE000u) | 0x30000000u), 0);
+    const double a = (double)bf16lo(w[i]), b = (double)bf16hi(w[i]);
     ss = __fma_rn(b, b, __fma_rn(a, a, ss));
   }
   return ss;
